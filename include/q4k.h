@@ -71,7 +71,7 @@ typedef enum {
 } q4k_status;
 
 enum { Q4K_ACT_NONE = 0, Q4K_ACT_SWIGLU = 1 };
-enum { Q4K_OP_GEMM = 1, Q4K_OP_ROUTE = 2, Q4K_OP_GROUPED = 3, Q4K_OP_GEMV = 4 };
+enum { Q4K_OP_GEMM = 1, Q4K_OP_ROUTE = 2, Q4K_OP_GROUPED = 3, Q4K_OP_GEMV = 4, Q4K_OP_MOE_I8 = 5 };
 
 /* Dequantise `nblocks` consecutive Q4_K blocks (hipEngine 0.3.0 README,
  * "GGUF Support": the Q4_K quant reader).
@@ -326,10 +326,58 @@ q4k_status moe_route_permute_hidden(const uint16_t* X, const uint16_t* W_router,
                                     int32_t* expert_offsets, int32_t* perm, int32_t* inv_perm,
                                     int32_t* row_token, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- the 8-bit integer lane: int8 codes with one fp32 scale per row --------------
+ * A row of K values is held as int8 codes q and one fp32 scale s, standing for s * q:
+ * activations with a scale per token, weights with a scale per output channel. K % 16
+ * == 0 in all three entry points (a row then starts on a 16-byte boundary). They have no
+ * counterpart on the pages; they stand beside the Q8 lane and the bf16-weight GEMM.
+ *
+ * i8_quantize: bf16 rows to codes and scales (activations before i8_gemm; at load time
+ * the weights of i8_gemm and moe_i8_layer, e.g. from q4k_dequant's bf16 output).
+ *   X bf16 [M][K]; Q int8 [M][K]; scale fp32 [M].
+ *   amax = max_k |x|, scale = RN_fp32(amax / 127), q = 127 x / amax rounded to the
+ *   nearest integer, ties to even (of the exact quotient). A row of zeros: scale 0,
+ *   codes 0. A row with an infinity or a NaN: scale NaN, codes 0.
+ * M == 0 is a no-op. */
+q4k_status i8_quantize(const uint16_t* X, int M, int K, int8_t* Q, float* scale, void* stream);
+
+/* Matrix product in 8-bit integers on tcgen05 tensor cores, any M >= 1.
+ *   acc = sum_k W[n][k] * X[m][k] in int32 (exact),
+ *   y[m][n] = RN(RN(float(acc) * x_scale[m]) * w_scale[n]) in fp32.
+ *   W int8 [N][K], w_scale fp32 [N], X int8 [M][K], x_scale fp32 [M]; codes -128..127.
+ *   act == Q4K_ACT_NONE:   Y [M][N], fp32, or bf16 (nearest even) when out_bf16 != 0.
+ *   act == Q4K_ACT_SWIGLU: Y bf16 [M][N/2] (out_bf16 must be set), SiLU(g) * u with
+ *     g = y of rows 0..N/2-1 of W, u = y of rows N/2..N-1.
+ * The sums are exact, so a result does not depend on the batch or the launch shape.
+ * K <= 131056 (the sums fit int32); any N. M == 0 or N == 0 is a no-op. */
+q4k_status i8_gemm(const int8_t* W, const float* w_scale, const int8_t* X, const float* x_scale, void* Y, int M, int N,
+                   int K, int act, int out_bf16, void* stream);
+
+/* A whole mixture-of-experts layer for 1 <= M <= 32 tokens in two launches: routing,
+ * the selected experts' gate and up products with SwiGLU, their down products, the
+ * weighted combine and the residual add.
+ *   logits    fp32 [M][E]; routing as moe_route_permute (top-k by logit, equal logits to
+ *             the lower id, softmax over the selected ones). A NaN logit ranks below all
+ *             others.
+ *   W_gate_up int8 [E][2F][H] (gate rows first), s_gate_up fp32 [E][2F];
+ *   W_down    int8 [E][H][F], s_down fp32 [E][H];
+ *   X         bf16 [M][H]; residual fp32 [M][H] or NULL, may be Y; Y fp32 [M][H]:
+ *     Y[t] = residual[t] + sum_j p[t][j] * s_down * (W_down[e] h),
+ *     h = SiLU(g) * u, g and u = s_gate_up * (W_gate_up[e] X[t]).
+ * The activations stay bf16 and h fp32 (no 8-bit rounding inside); sums in fp32, in an
+ * order that depends on the sizes and the routing alone.
+ *   ws/ws_bytes: device scratch of q4k_workspace_bytes(Q4K_OP_MOE_I8, M, H, F, E, topk)
+ *   bytes; calls (and captured graphs) that share it must be ordered on one stream.
+ * H % 16 == 0, F % 16 == 0, E <= 1024, topk <= min(E, 16). M == 0 is a no-op. */
+q4k_status moe_i8_layer(const float* logits, int M, int E, int topk, const int8_t* W_gate_up, const float* s_gate_up,
+                        const int8_t* W_down, const float* s_down, int H, int F, const uint16_t* X,
+                        const float* residual, float* Y, void* ws, size_t ws_bytes, void* stream);
+
 /* Bytes of device workspace an entry point needs for these sizes
  * (Q4K_OP_ROUTE: moe_route_permute with M tokens and E experts;
  *  Q4K_OP_GEMV: q4k_gemv with M tokens and K inputs;
  *  Q4K_OP_GROUPED: moe_q4k_grouped with M = rows and K inputs;
+ *  Q4K_OP_MOE_I8: moe_i8_layer with M tokens, N = H and K = F;
  *  Q4K_OP_GEMM: 0). */
 size_t q4k_workspace_bytes(int op, int M, int N, int K, int E, int topk);
 

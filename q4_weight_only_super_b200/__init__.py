@@ -18,12 +18,13 @@ __all__ = [
     "moe_route_permute",
     "moe_route_permute_noalloc", "moe_route_permute_hidden", "moe_route_gate_up",
     "moe_q4k_grouped", "moe_combine", "moe_combine_residual", "q4k_workspace_bytes", "q4k_last_device_status",
+    "i8_quantize", "i8_gemm", "moe_i8_layer",
     "q4k_test_wait_fault",
-    "ACT_NONE", "ACT_SWIGLU", "OP_GEMM", "OP_ROUTE", "OP_GROUPED", "OP_GEMV", "EXPORTS",
+    "ACT_NONE", "ACT_SWIGLU", "OP_GEMM", "OP_ROUTE", "OP_GROUPED", "OP_GEMV", "OP_MOE_I8", "EXPORTS",
 ]
 
 ACT_NONE, ACT_SWIGLU = 0, 1
-OP_GEMM, OP_ROUTE, OP_GROUPED, OP_GEMV = 1, 2, 3, 4
+OP_GEMM, OP_ROUTE, OP_GROUPED, OP_GEMV, OP_MOE_I8 = 1, 2, 3, 4, 5
 BLOCK_BYTES = 144
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libq4k.so")
 
@@ -48,6 +49,9 @@ EXPORTS = {
     "moe_route_gate_up": (_i, [_p, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _i, _i, _p, _p, _p]),
     "moe_combine": (_i, [_p, _p, _p, _i, _i, _i, _p, _p]),
     "moe_combine_residual": (_i, [_p, _p, _p, _p, _i, _i, _i, _p, _p]),
+    "i8_quantize": (_i, [_p, _i, _i, _p, _p, _p]),
+    "i8_gemm": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p]),
+    "moe_i8_layer": (_i, [_p, _i, _i, _i, _p, _p, _p, _p, _i, _i, _p, _p, _p, _p, _sz, _p]),
     "q4k_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "q4k_last_device_status": (_i, [_p]),
     "q4k_test_wait_fault": (_i, [_i, ctypes.c_uint64]),
@@ -350,6 +354,136 @@ def moe_combine_residual(O, inv_perm, topk_w, residual, M: int, topk: int, H: in
         Y = torch.empty(M, H, dtype=torch.float32, device=O.device)
     _check("moe_combine_residual", lib().moe_combine_residual(_ptr(O), _ptr(inv_perm), _ptr(topk_w), _ptr(residual),
                                                               M, topk, H, _ptr(Y), _stream(stream)))
+    return Y
+
+
+def _need(fn, name, t, dtypes, shape, device):
+    """An operand of the int8 lane: a contiguous CUDA tensor of the right type, shape and device."""
+    if t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{fn}: {name} must be a contiguous {' or '.join(str(d) for d in dtypes)} tensor of shape "
+                         f"{shape} on {device}; got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_I8, _F32 = (torch.int8,), (torch.float32,)
+
+
+class _On:
+    """The device and stream a call of the int8 lane runs on: the operands' device made
+    current, and what the call allocates taken from its own stream's pool."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.ctx = device, stream, None
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.device)
+            self.ctx.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        s = self.stream
+        if isinstance(s, int):
+            s = torch.cuda.ExternalStream(s, device=self.device) if s else torch.cuda.default_stream(self.device)
+        with torch.cuda.stream(s):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def _cuda_device(fn, t):
+    if t.device.type != "cuda":
+        raise ValueError(f"{fn}: the operands must be CUDA tensors; got one on {t.device}")
+    return t.device
+
+
+def i8_quantize(X, Q=None, scale=None, stream=None):
+    """bf16 rows X [M][K] -> (int8 codes [M][K], fp32 scales [M]); see include/q4k.h."""
+    dev = _cuda_device("i8_quantize", X)
+    if X.dim() != 2:
+        raise ValueError(f"i8_quantize: X must have two dimensions; got shape {tuple(X.shape)}")
+    M, K = X.shape
+    _need("i8_quantize", "X", X, _BF16, (M, K), dev)
+    on = _On(dev, stream)
+    with on as st:
+        if Q is None:
+            Q = on.empty((M, K), torch.int8)
+        else:
+            _need("i8_quantize", "Q", Q, _I8, (M, K), dev)
+        if scale is None:
+            scale = on.empty((M,), torch.float32)
+        else:
+            _need("i8_quantize", "scale", scale, _F32, (M,), dev)
+        _check("i8_quantize", lib().i8_quantize(X.data_ptr(), M, K, Q.data_ptr(), scale.data_ptr(), st))
+    return Q, scale
+
+
+def i8_gemm(W, w_scale, X, x_scale, act: int = ACT_NONE, out_bf16: bool = False, Y=None, stream=None):
+    """Y[m][n] = x_scale[m] * w_scale[n] * (X[m] . W[n]) from int8 W [N][K] and X [M][K];
+    fp32, or bf16 with out_bf16 (or a bf16 Y). ACT_SWIGLU: bf16 [M][N/2], SiLU of the first
+    N/2 channels times the others."""
+    dev = _cuda_device("i8_gemm", W)
+    if W.dim() != 2 or X.dim() != 2:
+        raise ValueError(f"i8_gemm: W and X must have two dimensions; got {tuple(W.shape)}, {tuple(X.shape)}")
+    N, K = W.shape
+    M = X.shape[0]
+    _need("i8_gemm", "W", W, _I8, (N, K), dev)
+    _need("i8_gemm", "w_scale", w_scale, _F32, (N,), dev)
+    _need("i8_gemm", "X", X, _I8, (M, K), dev)
+    _need("i8_gemm", "x_scale", x_scale, _F32, (M,), dev)
+    swiglu = act == ACT_SWIGLU
+    on = _On(dev, stream)
+    with on as st:
+        shape = (M, N // 2 if swiglu else N)
+        if Y is None:
+            Y = on.empty(shape, torch.bfloat16 if swiglu or out_bf16 else torch.float32)
+        else:
+            _need("i8_gemm", "Y", Y, (torch.bfloat16,) if swiglu or out_bf16 else (torch.float32, torch.bfloat16),
+                  shape, dev)
+        _check("i8_gemm", lib().i8_gemm(W.data_ptr(), w_scale.data_ptr(), X.data_ptr(), x_scale.data_ptr(),
+                                        Y.data_ptr(), M, N, K, act, int(Y.dtype == torch.bfloat16), st))
+    return Y
+
+
+def moe_i8_layer(logits, topk: int, W_gate_up, s_gate_up, W_down, s_down, X, residual=None, Y=None, ws=None,
+                 stream=None):
+    """A whole mixture-of-experts layer for up to 32 tokens over int8 experts, in two launches
+    (see include/q4k.h): logits fp32 [M][E], W_gate_up int8 [E][2F][H], W_down int8 [E][H][F]
+    with fp32 scales [E][2F] and [E][H], X bf16 [M][H]; returns Y fp32 [M][H]."""
+    fn = "moe_i8_layer"
+    dev = _cuda_device(fn, W_gate_up)
+    if logits.dim() != 2 or W_down.dim() != 3:
+        raise ValueError(f"{fn}: logits must have two dimensions and W_down three; got {tuple(logits.shape)}, "
+                         f"{tuple(W_down.shape)}")
+    M, E = logits.shape
+    _, H, F = W_down.shape
+    _need(fn, "logits", logits, _F32, (M, E), dev)
+    _need(fn, "W_gate_up", W_gate_up, _I8, (E, 2 * F, H), dev)
+    _need(fn, "s_gate_up", s_gate_up, _F32, (E, 2 * F), dev)
+    _need(fn, "W_down", W_down, _I8, (E, H, F), dev)
+    _need(fn, "s_down", s_down, _F32, (E, H), dev)
+    _need(fn, "X", X, _BF16, (M, H), dev)
+    if residual is not None:
+        _need(fn, "residual", residual, _F32, (M, H), dev)
+    on = _On(dev, stream)
+    with on as st:
+        if Y is None:
+            Y = on.empty((M, H), torch.float32)
+        else:
+            _need(fn, "Y", Y, _F32, (M, H), dev)
+        if ws is None:
+            ws = on.empty((max(16, q4k_workspace_bytes(OP_MOE_I8, M, H, F, E, topk)),), torch.uint8)
+        elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev:
+            raise ValueError(f"{fn}: ws must be a contiguous torch.uint8 tensor on {dev}")
+        _check(fn, lib().moe_i8_layer(logits.data_ptr(), M, E, topk, W_gate_up.data_ptr(), s_gate_up.data_ptr(),
+                                      W_down.data_ptr(), s_down.data_ptr(), H, F, X.data_ptr(),
+                                      None if residual is None else residual.data_ptr(), Y.data_ptr(),
+                                      ws.data_ptr(), ws.numel(), st))
     return Y
 
 

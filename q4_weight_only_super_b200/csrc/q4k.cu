@@ -14,7 +14,10 @@
 #include "gemv_sk.cuh"
 #include "gemv_sk6.cuh"
 #include "gemv_skg.cuh"
+#include "i8_gemm.cuh"
+#include "i8_quant.cuh"
 #include "moe.cuh"
+#include "moe_i8.cuh"
 
 using namespace q4k;
 
@@ -419,6 +422,118 @@ q4k_status noalloc_route_scratch(int32_t** out) {
   return Q4K_OK;
 }
 
+// ------------------------------------------------------------ int8 products ----
+
+// Shared memory of one product CTA: the whole SM's for tiles of many tokens, half of it
+// (two CTAs per SM) for narrow ones, whose accumulators then fit half the TMEM too.
+constexpr size_t kI8Smem[2] = {232448, kGemvTwoPerSm};
+constexpr size_t kI8TailBytes = 256 + 4 * kI8MaxNT * sizeof(float);
+
+// g_i8_fit[d][h][c]: clusters of c product CTAs (h: two CTAs per SM) resident at once.
+std::atomic<int> g_i8_fit[kMaxDevices][2][9];
+
+template <typename F>
+q4k_status i8_launch(F* k, const CUtensorMap& tw, const CUtensorMap& tx, const I8GemmParams& p, int grid, int cluster,
+                     size_t smem, std::atomic<size_t> (&smem_set)[kMaxDevices], cudaStream_t s, int* fit = nullptr) {
+  if (ensure_smem(k, kI8Smem[0], smem_set) != cudaSuccess) return launch_status(cudaErrorUnknown);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(kI8Threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (fit) {
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(fit, k, &cfg) != cudaSuccess || *fit <= 0) {
+      cudaGetLastError();
+      *fit = 0;
+    }
+    return Q4K_OK;
+  }
+  return launch_status(cudaLaunchKernelEx(&cfg, k, tw, tx, p));
+}
+
+std::atomic<size_t> g_i8_smem_fit[kMaxDevices];
+
+int i8_cluster_fit(int halved, int c) {
+  const int dev = current_device();
+  if (dev < 0 || dev >= kMaxDevices) return 0;
+  int v = g_i8_fit[dev][halved][c].load();
+  if (v <= 0) {
+    CUtensorMap none = {};
+    i8_launch(i8_gemm_kernel<false, false, true>, none, none, I8GemmParams{}, 64 * c, c, kI8Smem[halved],
+              g_i8_smem_fit, nullptr, &v);
+    g_i8_fit[dev][halved][c].store(v);
+  }
+  return v;
+}
+
+template <bool SWIGLU, bool BF16>
+q4k_status i8_gemm_t(const int8_t* W, const int8_t* X, I8GemmParams p, cudaStream_t s) {
+  const int sms = sm_count();
+  if (sms <= 0) return Q4K_ERR_CUDA;
+  // token tiles of equal width, at most 256
+  p.m_tiles = (p.M + kI8MaxNT - 1) / kI8MaxNT;
+  p.nt = ((p.M + p.m_tiles - 1) / p.m_tiles + 15) / 16 * 16;
+  const int rows = SWIGLU ? p.N / 2 : p.N, tile_rows = SWIGLU ? kI8Rows / 2 : kI8Rows;
+  p.n_tiles = (rows + tile_rows - 1) / tile_rows;
+  if ((int64_t)p.n_tiles * p.m_tiles > 0x7fffffffLL / 8) return Q4K_ERR_UNSUPPORTED;
+  const int tiles = p.n_tiles * p.m_tiles;
+  const int nk = (p.K + kI8KB - 1) / kI8KB;
+  p.tstride = (p.nt + 31) / 32 * 32;
+  const size_t stage = kI8ATile + (size_t)p.nt * kI8KB;
+  const int halved = p.nt <= 128;
+  const size_t smem = kI8Smem[halved];
+  p.stages = std::min<int>(kI8MaxStages, (int)((smem - 1024 - kI8TailBytes) / stage));
+  p.tail = (int)(p.stages * stage);
+  // K split over the largest cluster with which all tiles are resident at once
+  int c = 1;
+  for (int t = std::min(8, nk); t > 1; --t)
+    if (i8_cluster_fit(halved, t) >= tiles) {
+      c = t;
+      break;
+    }
+  p.csplit = c;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < (c > 1 ? 1 : 2) * p.tstride) p.tmem_cols *= 2;
+  CUtensorMap tw, tx;
+  if (!make_tmap_i8(&tw, W, p.N, p.K, SWIGLU ? 16 : kI8Rows) || !make_tmap_i8(&tx, X, p.M, p.K, p.nt))
+    return Q4K_ERR_CUDA;
+  static std::atomic<size_t> smem_set[2][kMaxDevices];
+  if (c > 1)
+    return i8_launch(i8_gemm_kernel<SWIGLU, BF16, true>, tw, tx, p, tiles * c, c, smem, smem_set[1], s);
+  return i8_launch(i8_gemm_kernel<SWIGLU, BF16, false>, tw, tx, p, std::min(tiles, sms * (halved + 1)), 1, smem,
+                   smem_set[0], s);
+}
+
+template <int PL>
+q4k_status launch_mi8(const Mi8Params& p, cudaStream_t s) {
+  auto* k = mi8_gate_up_kernel<PL>;
+  static std::atomic<int> per_sm[kMaxDevices];
+  const int dev = current_device();
+  if (dev < 0 || dev >= kMaxDevices || sm_count() <= 0) return Q4K_ERR_CUDA;
+  int n = per_sm[dev].load();
+  if (n <= 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, 32 * kMi8Warps1, 0) != cudaSuccess || n <= 0)
+      return launch_status(cudaErrorUnknown);
+    per_sm[dev].store(n);
+  }
+  const int64_t most = (int64_t)p.M * p.topk * (p.F / 8);  // units, were every group one row
+  const q4k_status st = launch_pdl(k, dim3((unsigned)std::min<int64_t>(most, (int64_t)n * sm_count())),
+                                   dim3(32 * kMi8Warps1), s, p);
+  if (st != Q4K_OK) return st;
+  return launch_pdl(mi8_down_kernel, dim3((unsigned)(p.H / 16)), dim3(32 * kMi8Warps2), s, p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -658,9 +773,84 @@ q4k_status bf16w_gemm(const uint16_t* Wb, const uint16_t* X, float* Y, int M, in
   return launch_gemm_tc_bf16w(p, static_cast<cudaStream_t>(stream));
 }
 
+q4k_status i8_quantize(const uint16_t* X, int M, int K, int8_t* Q, float* scale, void* stream) {
+  if (M < 0 || K <= 0 || K % 16) return Q4K_ERR_SHAPE;
+  if (M == 0) return Q4K_OK;
+  if (!X || !Q || !scale) return Q4K_ERR_NULL;
+  if (!aligned16(X) || !aligned16(Q) || !aligned16(scale)) return Q4K_ERR_ALIGN;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto rows = [&](int per) { return dim3((unsigned)((M + (int64_t)per - 1) / per)); };
+  // the fewest threads that hold a row in registers: more rows in flight per SM
+  constexpr int kHold = 8 * kI8QVec;
+  if (K <= 32 * kHold) return launch_pdl(i8_quantize_kernel<32>, rows(8), dim3(256), s, X, M, K, Q, scale);
+  if (K <= 128 * kHold) return launch_pdl(i8_quantize_kernel<128>, rows(2), dim3(256), s, X, M, K, Q, scale);
+  if (K <= 256 * kHold) return launch_pdl(i8_quantize_kernel<256>, rows(1), dim3(256), s, X, M, K, Q, scale);
+  if (K <= 512 * kHold) return launch_pdl(i8_quantize_kernel<512>, rows(1), dim3(512), s, X, M, K, Q, scale);
+  return launch_pdl(i8_quantize_kernel<1024>, rows(1), dim3(1024), s, X, M, K, Q, scale);
+}
+
+q4k_status i8_gemm(const int8_t* W, const float* w_scale, const int8_t* X, const float* x_scale, void* Y, int M, int N,
+                   int K, int act, int out_bf16, void* stream) {
+  if (M < 0 || N < 0 || K <= 0 || K % 16) return Q4K_ERR_SHAPE;
+  if (act != Q4K_ACT_NONE && act != Q4K_ACT_SWIGLU) return Q4K_ERR_UNSUPPORTED;
+  if (act == Q4K_ACT_SWIGLU && N % 2) return Q4K_ERR_SHAPE;
+  if (M == 0 || N == 0) return Q4K_OK;
+  if (!W || !w_scale || !X || !x_scale || !Y) return Q4K_ERR_NULL;
+  if (!aligned16(W) || !aligned16(w_scale) || !aligned16(X) || !aligned16(x_scale) || !aligned16(Y))
+    return Q4K_ERR_ALIGN;
+  if (K > kI8MaxK || (act == Q4K_ACT_SWIGLU && !out_bf16)) return Q4K_ERR_UNSUPPORTED;
+  I8GemmParams p = {};
+  p.xs = x_scale;
+  p.ws = w_scale;
+  p.Y = Y;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (act == Q4K_ACT_SWIGLU) return i8_gemm_t<true, true>(W, X, p, s);
+  return out_bf16 ? i8_gemm_t<false, true>(W, X, p, s) : i8_gemm_t<false, false>(W, X, p, s);
+}
+
+q4k_status moe_i8_layer(const float* logits, int M, int E, int topk, const int8_t* W_gate_up, const float* s_gate_up,
+                        const int8_t* W_down, const float* s_down, int H, int F, const uint16_t* X,
+                        const float* residual, float* Y, void* ws, size_t ws_bytes, void* stream) {
+  if (M < 0 || E <= 0 || topk <= 0 || H <= 0 || F <= 0 || H % 16 || F % 16) return Q4K_ERR_SHAPE;
+  if (M > kMi8MaxM || E > kMaxE || topk > kMaxTopk || topk > E) return Q4K_ERR_UNSUPPORTED;
+  if (F > 0x7fffffff / (kMi8MaxRows / 8)) return Q4K_ERR_UNSUPPORTED;  // units in 32 bits
+  if (M == 0) return Q4K_OK;
+  if (!logits || !W_gate_up || !s_gate_up || !W_down || !s_down || !X || !Y || !ws) return Q4K_ERR_NULL;
+  if (!aligned16(logits) || !aligned16(W_gate_up) || !aligned16(s_gate_up) || !aligned16(W_down) ||
+      !aligned16(s_down) || !aligned16(X) || !aligned16(Y) || !aligned16(ws) || (residual && !aligned16(residual)))
+    return Q4K_ERR_ALIGN;
+  if (ws_bytes < q4k_workspace_bytes(Q4K_OP_MOE_I8, M, H, F, E, topk)) return Q4K_ERR_WORKSPACE;
+  Mi8Params p = {};
+  p.logits = logits;
+  p.Wgu = W_gate_up;
+  p.sgu = s_gate_up;
+  p.Wd = W_down;
+  p.sd = s_down;
+  p.X = X;
+  p.residual = residual;
+  p.Y = Y;
+  p.plan = static_cast<Mi8Plan*>(ws);
+  p.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + (mi8_ws_bytes(0, 0, 0)));
+  p.M = M;
+  p.E = E;
+  p.topk = topk;
+  p.H = H;
+  p.F = F;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (E <= 128) return launch_mi8<4>(p, s);
+  if (E <= 256) return launch_mi8<8>(p, s);
+  return launch_mi8<32>(p, s);
+}
+
 size_t q4k_workspace_bytes(int op, int M, int N, int K, int E, int topk) {
   (void)N;
-  (void)topk;
+  if (op == Q4K_OP_MOE_I8) {
+    if (M <= 0 || K <= 0 || topk <= 0) return 0;
+    return mi8_ws_bytes(M, topk, K);
+  }
   if (op == Q4K_OP_ROUTE) {
     if (M <= 0 || E <= 0) return 0;
     const size_t tiles = (size_t)(M + kRouteTokPerCta - 1) / kRouteTokPerCta;
