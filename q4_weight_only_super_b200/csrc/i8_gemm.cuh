@@ -51,7 +51,19 @@ struct I8GemmParams {
   int tstride;   // TMEM columns between the two accumulators (a multiple of 32)
   int tmem_cols; // columns to allocate: two accumulators (SPLIT: one), a power of two
   int tail;      // shared-memory offset of barriers and scales
+  int boxed;     // SwiGLU: the weights' map is make_tmap_gate_up's
 };
+
+// The 64 gate and 64 up rows of a SwiGLU tile as one 5-D box: for each 16 rows of the
+// gate (coordinate r16 of 16-row groups), those and the 16 matching up rows.
+__device__ __forceinline__ void tma_load_gate_up(uint32_t dst, const CUtensorMap* map, int x, int r16, int e,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(r16), "r"(e), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ void umma_i8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -84,6 +96,19 @@ __device__ __forceinline__ void st_cluster_s32(uint32_t saddr, uint32_t rank, in
       "r"(rank), "r"(v)
       : "memory");
 }
+
+// A place in a ring of stages, and the parity of its pass (the roles' single threads pay
+// for every instruction, so no division by the runtime stage count).
+struct I8Ring {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+};
 
 template <bool BF16>
 __device__ __forceinline__ void i8_store(void* Y, int64_t at, float v) {
@@ -158,23 +183,28 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
   const int k0 = SPLIT ? (int)((int64_t)nk_all * rank / p.csplit) : 0;
   const int nk = SPLIT ? (int)((int64_t)nk_all * (rank + 1) / p.csplit) - k0 : nk_all;  // >= 1
   const int half = p.N / 2;
+  const uint64_t limit = *const_cast<volatile unsigned long long*>(&g_wait_limit_ns);
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (lane == 0) {
       const int drop = g_test_drop_stage;  // test hook; -1 in normal use
       int it = 0;
+      I8Ring at;
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += step) {
         const int m0 = tile % p.m_tiles * p.nt, nti = tile / p.m_tiles;
-        for (int k = 0; k < nk; ++k, ++it) {
-          const int s = it % p.stages, u = it / p.stages;
-          if (u >= 1 && !(ok = mbar_wait(bar_empty(s), (u - 1) & 1, abort_flag))) break;
+        for (int k = 0; k < nk; ++k, ++it, at.next(p.stages)) {
+          const int s = at.s;
+          // (a barrier's phase before its first counts as complete)
+          if (!(ok = mbar_wait_l(bar_empty(s), at.parity ^ 1, abort_flag, limit))) break;
           if (it == drop) continue;  // test hook: this stage never arrives
           mbar_arrive_expect_tx(bar_full(s), stage_bytes);
           const uint32_t a_dst = sbase + s * stage_bytes;
           const int x = (k0 + k) * kI8KB;
-          if (SWIGLU) {
+          if (SWIGLU && p.boxed) {
+            tma_load_gate_up(a_dst, &tmap_w, x, nti * 4, 0, bar_full(s));
+          } else if (SWIGLU) {
             const int f0 = nti * (kI8Rows / 2);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -197,22 +227,23 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
       const uint32_t idesc = i8_idesc(kI8Rows, p.nt);
-      int it = 0, done = 0;
+      int done = 0;
+      I8Ring at;
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += step, ++done) {
         const int a = done & 1;
-        if (done >= 2 && !(ok = mbar_wait(bar_tempty(a), (done / 2 - 1) & 1, abort_flag))) break;
+        if (done >= 2 && !(ok = mbar_wait_l(bar_tempty(a), (done / 2 - 1) & 1, abort_flag, limit))) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(a * p.tstride);
-        for (int k = 0; k < nk; ++k, ++it) {
-          const int s = it % p.stages;
-          if (!(ok = mbar_wait(bar_full(s), (it / p.stages) & 1, abort_flag))) break;
+        for (int k = 0; k < nk; ++k, at.next(p.stages)) {
+          if (!(ok = mbar_wait_l(bar_full(at.s), at.parity, abort_flag, limit))) break;
           tc_fence_after();
-          const uint32_t a0 = sbase + s * stage_bytes, b0 = a0 + kI8ATile;
+          const uint32_t a0 = sbase + at.s * stage_bytes;
+          const uint64_t ad = umma_desc_sw128(a0), bd = umma_desc_sw128(a0 + kI8ATile);
 #pragma unroll
-          for (int kk = 0; kk < kI8KB / 32; ++kk)
-            umma_i8(d, umma_desc_sw128(a0 + kk * 32), umma_desc_sw128(b0 + kk * 32), idesc, (k | kk) != 0);
-          umma_commit(bar_empty(s));
+          for (int kk = 0; kk < kI8KB / 32; ++kk)  // 32 bytes of K on: 2 in the descriptors' units
+            umma_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
+          umma_commit(bar_empty(at.s));
         }
         if (ok) umma_commit(bar_tfull(a));
       }
@@ -233,7 +264,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
       const int r = i8_row<SWIGLU>(nti, q, lane, &up);
       const float w = r < rows ? p.ws[up ? half + r : r] : 0.f;
       __syncwarp();
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_tfull(a), (done / 2) & 1, abort_flag))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_l(bar_tfull(a), (done / 2) & 1, abort_flag, limit))) break;
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * p.tstride);
       for (int c = 0; c < mcount; c += 16) {
@@ -270,7 +301,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
     int32_t* part = reinterpret_cast<int32_t*>(smem);  // [csplit][per][128]: the stages are free by then
     const int q = warp & 3;
     bool ok = true;
-    if (warp >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar_tfull(0), 0, abort_flag));
+    if (warp >= 2) ok = __all_sync(0xffffffffu, mbar_wait_l(bar_tfull(0), 0, abort_flag, limit));
     __syncwarp();
     cluster_barrier();  // no CTA's MMAs read its stages any more
     if (warp >= 2 && ok) {
@@ -345,6 +376,22 @@ inline bool make_tmap_i8(CUtensorMap* m, const void* base, int64_t rows, int K, 
   cuuint32_t box[2] = {(cuuint32_t)kI8KB, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// int8 gate and up rows [E][2][F][K], F % 16 == 0, viewed as [E][F / 16][2][16][K]: one box
+// is 4 groups of 16 gate rows, each followed by the 16 matching up rows. (Sixteen-row boxes,
+// eight of them per stage, kept the one producing thread busy for ~700 cycles a stage.)
+inline bool make_tmap_gate_up(CUtensorMap* m, const void* base, int E, int F, int K) {
+  auto enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t k = (cuuint64_t)K, f = (cuuint64_t)F;
+  cuuint64_t dims[5] = {k, 16, 2, f / 16, (cuuint64_t)E};
+  cuuint64_t strides[4] = {k, f * k, 16 * k, 2 * f * k};
+  cuuint32_t box[5] = {(cuuint32_t)kI8KB, 16, 2, 4, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

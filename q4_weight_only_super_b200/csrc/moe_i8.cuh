@@ -5,367 +5,555 @@
 //   h_tj       = silu(g) * u,  g, u = s_gate_up[e] * (W_gate_up[e] X_t)      (kernel 1)
 //   Y_t        = residual_t + sum_j p_tj * s_down[e] * (W_down[e] h_tj)      (kernel 2)
 //
-// A few tokens select experts whose weights are each read for one or two rows: the weight
-// bytes bound the layer, so the activations stay bf16 (nothing would be saved by 8-bit
-// ones) and the weights go from global memory into registers in long contiguous runs, are
-// converted there to bf16 (exact) and multiplied by mma.sync m16n8k16 with fp32 sums.
-//
-//  * MMA operands without shuffles: K may be permuted as long as both operands agree, so
-//    lane (g, i) of a warp takes 16 contiguous bytes of weight row g, k = 64c + 16i .., as
-//    its A fragments of four MMAs, and the same 16 activations of token g as its B ones.
-//  * Kernel 1: a unit is 8 gate rows and the 8 matching up rows of one expert (an MMA's 16
-//    rows, so a gate and its up value meet in one lane) times up to 8 of its tokens. Units
-//    go round-robin over the CTAs; the four warps of a CTA split K.
-//  * h leaves kernel 1 as three bf16 planes (h = h0 + h1 + h2, 8 of
-//    its 24 bits each, exact); kernel 2 adds three MMAs into the same sums.
-//  * Kernel 2: a CTA owns 16 output columns and runs over all experts that were selected,
-//    so the combine needs no exchange between CTAs and no atomics: each warp adds its
-//    experts' rows, weighted, to its own sums in shared memory, which are added in warp
-//    order at the end. The result is deterministic.
-//  * Routing (a warp per token) runs in every CTA of kernel 1; CTA 0 leaves the list of
-//    (expert, rows) groups and the rows' tokens and weights for kernel 2.
+// A few tokens select experts whose weights are each read for one or two rows, so the
+// layer is bound by reading the weights, and nothing would be saved by activations of 8
+// bits. But the tensor cores take int8 weights as they are only with int8 activations:
+// a row of activations is therefore held as 24-bit fixed point, one scale per row, in three
+// signed base-256 digits, each a column of its own in the MMA:
+//   x = v / S,  v = rint(x S) = 65536 d0 + 256 d1 + d2,
+//   W x = (65536 (W d0) + 256 (W d1) + W d2) / S     with int32 sums, exact.
+// That keeps what fp32 sums would (X: S is a power of two, so a bf16 value within 2^14 of
+// its row's largest is exact; h: to 2^-23 of its row's largest), costs no instruction per
+// weight, and makes the sums independent of their order. mma.sync kernels that converted
+// the weights to bf16 in registers were measured at 188 us for 32 tokens (128 experts, top-8, H = 2048, F =
+// 768), bound by their ~100 instructions per KB of weights and their latencies.
+//   warp 0      TMA producer: 128 weight rows x 128 bytes of K per stage (128-byte swizzle).
+//   warp 1      TMEM; one lane issues tcgen05.mma kind::i8 (M=128, N = 4 columns per row of
+//               activations: three digits and one that nobody reads, rounded up to 16).
+//   warps 2-5   epilogue: a thread owns a weight row (output channel).
+//   warps 6-9   digits: each takes every fourth stage, reads the rows' 128 activations from
+//               L2 and writes their digits in the layout that the MMA reads.
+// Kernel 1: a unit is one expert's 64 gate and the matching 64 up rows (16 of each per warp
+// of the epilogue, one shuffle brings a pair together); units go round-robin over the CTAs.
+// h leaves as fp32 with the largest magnitude of every 16 of a row. Kernel 2: a CTA owns
+// 128 output columns and every split-th expert: the weighted rows are summed in shared
+// memory, and the last CTA of a column tile to finish adds the splits' sums in their order
+// (a counter, but no atomics on results: deterministic).
+// Routing (a warp per token) runs in every CTA of both kernels: kernel 2 then starts its
+// weight stream before kernel 1 has ended (programmatic dependent launch) and waits for it
+// only before it reads h.
+// Every wait is bounded; on expiry the kernel latches Q4K_ERR_DEVICE_TIMEOUT, stops all
+// roles, drains its own copies (bounded), frees TMEM and returns.
 #pragma once
 #include "common.cuh"
 #include "gemm_tc.cuh"
+#include "i8_gemm.cuh"
 #include "moe.cuh"
 
 namespace q4k {
 
 constexpr int kMi8MaxM = 32;
 constexpr int kMi8MaxRows = kMi8MaxM * kMaxTopk;  // (token, slot) pairs
-constexpr int kMi8Warps1 = 4;   // kernel 1: warps of a CTA, splitting K
-constexpr int kMi8Warps2 = 16;  // kernel 2: warps of a CTA, splitting the experts
-constexpr int kMi8Batch = 8;    // 64-wide pieces of K that a lane holds in registers
-
-// The plan that kernel 1 leaves for kernel 2 at the start of the workspace.
-struct Mi8Plan {
-  int32_t groups;
-  int32_t pad[3];
-  int32_t group_expert[kMi8MaxRows];  // a group: up to 8 rows of one expert
-  int32_t group_row[kMi8MaxRows];     // its first row | number of rows << 16
-  int32_t row_token[kMi8MaxRows];     // rows sorted by (expert, token)
-  float row_weight[kMi8MaxRows];
-};
+constexpr int kMi8Warps = 10;
+constexpr int kMi8DigitWarps = 4;
+constexpr int kMi8MaxStages = 10;
+constexpr float kMi8Top = 8355711.f;  // 127 * 65536 + 127 * 256 + 127: the largest three digits hold
 
 struct Mi8Params {
   const float* logits;
-  const int8_t* Wgu;
   const float* sgu;
-  const int8_t* Wd;
   const float* sd;
   const uint16_t* X;
   const float* residual;  // may be null; may be Y
   float* Y;
-  Mi8Plan* plan;
-  uint16_t* h;  // [rows][3][F] bf16
+  float* h;        // [rows][F], rows sorted by (expert, token)
+  uint32_t* hmax;  // [rows][hparts]: bits of the largest |h| of each 16
+  float* part;     // kernel 2: [column tile][split][M][128]
+  int32_t* count;  // kernel 2: [column tile], splits that have arrived
   int M, E, topk, H, F;
+  int hparts;  // 4 per tile of kernel 1
+  int nb;      // columns that a stage has room for: 4 M rounded up to 16
+  int stages, tstride, tmem_cols;
+  int split;   // kernel 2: CTAs that share a column tile, taking the experts in turn
 };
 
-inline size_t mi8_ws_bytes(int M, int topk, int F) {
-  return ((sizeof(Mi8Plan) + 255) & ~(size_t)255) + (size_t)M * topk * 3 * (size_t)F * 2;
+inline int mi8_tiles(int F) { return (F + 63) / 64; }
+
+constexpr int kMi8MaxCtas = 256;  // kernel 2: column tiles x splits, where split > 1
+
+// h, hmax, counters, partial sums
+inline size_t mi8_ws_h(int M, int topk, int F) { return (size_t)M * topk * F * 4; }
+inline size_t mi8_ws_hmax(int M, int topk, int F) { return (size_t)M * topk * 16 * (size_t)mi8_tiles(F); }
+inline size_t mi8_ws_bytes(int M, int topk, int H, int F) {
+  const size_t tiles = (size_t)(H + kI8Rows - 1) / kI8Rows;
+  return mi8_ws_h(M, topk, F) + mi8_ws_hmax(M, topk, F) + (tiles + 3) / 4 * 16 +
+         (size_t)kMi8MaxCtas * M * kI8Rows * 4;
 }
 
 // Order of the logits as unsigned keys: -inf .. +inf, a NaN below them all, 0 for none.
 __device__ __forceinline__ uint32_t mi8_key(float v) { return v != v ? 1u : order_key(v); }
 
-// Top-k of one token by a whole warp: lane j < topk returns the j-th expert (higher logit
-// first, equal logits by the lower id) and its softmax weight over the selected ones.
+// Top-k of one token by a whole warp from its PL logits per lane (expert 32 i + lane), as
+// keys: the j-th expert (higher logit first, equal logits by the lower id) goes to out[j],
+// its key to keys[j] (shared memory). Each lane keeps its keys sorted, so that a round is
+// one reduction, one ballot and a shift in the winning lane.
 template <int PL>
-__device__ __forceinline__ void mi8_topk(const float* __restrict__ row, int E, int topk, int lane, int* id, float* w) {
-  uint32_t key[PL];
+__device__ __forceinline__ void mi8_topk(uint32_t (&key)[PL], int topk, int lane, uint16_t* out, uint32_t* keys) {
+  int idx[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = i * 32 + lane;
-    key[i] = e < E ? mi8_key(row[e]) : 0u;
-  }
-  uint32_t my_key = 0;
-  *id = 0;
-  for (int k = 0; k < topk; ++k) {
-    uint32_t best = 0;
-    int bi = 0;
+  for (int i = 0; i < PL; ++i) idx[i] = 32 * i + lane;
+  if constexpr (PL <= 8) {
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        bi = i;
+    for (int i = 1; i < PL; ++i)  // insertion: equal keys stay in order of id
+#pragma unroll
+      for (int j = i; j > 0; --j) {
+        const bool sw = key[j] > key[j - 1];
+        const uint32_t a = sw ? key[j] : key[j - 1], b = sw ? key[j - 1] : key[j];
+        const int c = sw ? idx[j] : idx[j - 1], d = sw ? idx[j - 1] : idx[j];
+        key[j - 1] = a, key[j] = b, idx[j - 1] = c, idx[j] = d;
       }
+  }
+  for (int k = 0; k < topk; ++k) {
+    uint32_t best = key[0];
+    int bi = idx[0];
+    if constexpr (PL > 8) {
+#pragma unroll
+      for (int i = 1; i < PL; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          bi = idx[i];
+        }
+    }
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(bi * 32 + lane) : 0xffffffffu);
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (e == (uint32_t)(i * 32 + lane)) key[i] = 0;
-    if (lane == k) {
-      my_key = top;
-      *id = (int)e;
+    const unsigned who = __ballot_sync(0xffffffffu, best == top);
+    bool mine = best == top;
+    if (who & (who - 1)) {  // (the same for all lanes)
+      const uint32_t lowest = __reduce_min_sync(0xffffffffu, mine ? (uint32_t)bi : 0xffffffffu);
+      mine = (uint32_t)bi == lowest;
     }
-  }
-  const float v = my_key == 1u ? __uint_as_float(0x7FC00000u) : key_value(my_key);
-  const float v0 = __shfl_sync(0xffffffffu, v, 0);
-  const float ek = lane < topk ? expf(v - v0) : 0.f;
-  float den = ek;
+    if (mine) {
+      out[k] = (uint16_t)bi;
+      keys[k] = top;
+      if constexpr (PL <= 8) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  *w = ek / den;
-}
-
-// Four int8 of a word to four bf16, exact: with b = q + 128 in the low mantissa bits of
-// 0x43xx the value is 256 + q for q < 0 and 2q + 256 otherwise (the top bit of b reaches the
-// exponent); less 256 that is q, or 2q, and the smaller of it and its half is q.
-__device__ __forceinline__ void i8x4_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t b = w ^ 0x80808080u;
-  const uint32_t p0 = __byte_perm(b, 0x43434343u, 0x4140), p1 = __byte_perm(b, 0x43434343u, 0x4342);
-  const __nv_bfloat162 c = __floats2bfloat162_rn(256.f, 256.f), half = __floats2bfloat162_rn(0.5f, 0.5f);
-  const __nv_bfloat162 g0 = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&p0), c);
-  const __nv_bfloat162 g1 = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&p1), c);
-  const __nv_bfloat162 r0 = __hmin2(g0, __hmul2(g0, half)), r1 = __hmin2(g1, __hmul2(g1, half));
-  lo = *reinterpret_cast<const uint32_t*>(&r0);
-  hi = *reinterpret_cast<const uint32_t*>(&r1);
-}
-
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// One 64-wide piece of K: A from rows g (u) and g + 8 (v) of 16 bytes a lane, B planes.
-template <int PLANES>
-__device__ __forceinline__ void mi8_piece(float (&acc)[4], const uint4& u, const uint4& v, const uint4 (&b)[PLANES][2]) {
-  const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i + 1 < PL; ++i) {
+          key[i] = key[i + 1];
+          idx[i] = idx[i + 1];
+        }
+        key[PL - 1] = 0;
+      } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t a0, a1, a2, a3;
-    i8x4_bf16(uw[j], a0, a2);
-    i8x4_bf16(vw[j], a1, a3);
-#pragma unroll
-    for (int pl = PLANES - 1; pl >= 0; --pl) {
-      const uint4& q = b[pl][j >> 1];
-      mma_bf16(acc, a0, a1, a2, a3, j & 1 ? q.z : q.x, j & 1 ? q.w : q.y);
+        for (int i = 0; i < PL; ++i)
+          if (idx[i] == bi) key[i] = 0;
+      }
     }
   }
 }
 
-__device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
+// The routing of all tokens, as every CTA of both kernels holds it: rows sorted by
+// (expert, token), the rows of one expert forming a group.
+template <int PL>
+struct Mi8Route {
+  unsigned tmask[32 * PL];  // tokens that selected expert e
+  int start[32 * PL];       // e's first row
+  uint16_t id[kMi8MaxRows];  // [token][slot]
+  uint32_t w[kMi8MaxRows];   // the logits' keys, then the weights' bits
+  uint16_t group_expert[kMi8MaxRows];
+  int group_row[kMi8MaxRows];  // first row | number of rows << 16
+  uint16_t row_token[kMi8MaxRows];
+  float row_weight[kMi8MaxRows];
+  int groups;
+};
 
 template <int PL>
-__global__ void __launch_bounds__(32 * kMi8Warps1, 4)
-mi8_gate_up_kernel(Mi8Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ unsigned tmask[32 * PL];          // tokens that selected expert e
-  __shared__ int s_id[kMi8MaxRows];            // [token][slot]
-  __shared__ float s_w[kMi8MaxRows];
-  __shared__ int start[32 * PL];               // expert's first row
-  __shared__ int g_expert[kMi8MaxRows], g_row[kMi8MaxRows];
-  __shared__ int s_token[kMi8MaxRows];         // row -> token
-  __shared__ int s_groups;
-  __shared__ float red[2][kMi8Warps1][16][8];
+__device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-
-  // ---- routing: who goes where ----
-  for (int e = threadIdx.x; e < 32 * PL; e += blockDim.x) tmask[e] = 0u;
+  for (int e = threadIdx.x; e < 32 * PL; e += 32 * kMi8Warps) r.tmask[e] = 0u;
   __syncthreads();
-  for (int t = warp; t < p.M; t += kMi8Warps1) {
-    int id;
-    float w;
-    mi8_topk<PL>(p.logits + (int64_t)t * p.E, p.E, p.topk, lane, &id, &w);
+  uint32_t next[PL];
+  auto load = [&](int t) {
+    const float* row = p.logits + (int64_t)t * p.E;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) next[i] = t < p.M && 32 * i + lane < p.E ? mi8_key(row[32 * i + lane]) : 0u;
+  };
+  load(warp);
+#pragma unroll 1
+  for (int t = warp; t < p.M; t += kMi8Warps) {
+    uint32_t key[PL];
+#pragma unroll
+    for (int i = 0; i < PL; ++i) key[i] = next[i];
+    load(t + kMi8Warps);  // under this token's rounds
+    uint16_t* id = r.id + t * p.topk;
+    uint32_t* w = r.w + t * p.topk;
+    mi8_topk<PL>(key, p.topk, lane, id, w);
+    __syncwarp();
+    // softmax over the selected: lane j has the j-th, the sum in a fixed butterfly order
+    const uint32_t k = w[min(lane, p.topk - 1)], k0 = w[0];
+    const float nan = __uint_as_float(0x7FC00000u);
+    const float v = k == 1u ? nan : key_value(k), v0 = k0 == 1u ? nan : key_value(k0);
+    const float ek = lane < p.topk ? expf(v - v0) : 0.f;
+    float den = ek;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     if (lane < p.topk) {
-      s_id[t * p.topk + lane] = id;
-      s_w[t * p.topk + lane] = w;
-      atomicOr(&tmask[id], 1u << t);
+      w[lane] = __float_as_uint(ek / den);
+      atomicOr(&r.tmask[id[lane]], 1u << t);
     }
   }
   __syncthreads();
-  if (warp == 0) {  // groups of up to 8 rows, experts in order
+  if (warp == 0) {
     int rows = 0, groups = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int c = __popc(tmask[e0 + lane]), n = (c + 7) / 8;
-      int rc = c, rn = n;  // inclusive scans
+      const int c = __popc(r.tmask[e0 + lane]);
+      int sum = c;  // inclusive scan
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, rc, o), b = __shfl_up_sync(0xffffffffu, rn, o);
-        if (lane >= o) {
-          rc += a;
-          rn += b;
-        }
+        const int a = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += a;
       }
-      start[e0 + lane] = rows + rc - c;
-      for (int i = 0; i < n; ++i) {
-        g_expert[groups + rn - n + i] = e0 + lane;
-        g_row[groups + rn - n + i] = (rows + rc - c + 8 * i) | min(8, c - 8 * i) << 16;
+      const unsigned some = __ballot_sync(0xffffffffu, c > 0);
+      r.start[e0 + lane] = rows + sum - c;
+      if (c > 0) {
+        const int grp = groups + __popc(some & ((1u << lane) - 1u));
+        r.group_expert[grp] = (uint16_t)(e0 + lane);
+        r.group_row[grp] = (rows + sum - c) | c << 16;
       }
-      rows += __shfl_sync(0xffffffffu, rc, 31);
-      groups += __shfl_sync(0xffffffffu, rn, 31);
+      rows += __shfl_sync(0xffffffffu, sum, 31);
+      groups += __popc(some);
     }
-    if (lane == 0) s_groups = groups;
+    if (lane == 0) r.groups = groups;
   }
   __syncthreads();
-  const int groups = s_groups;
-  for (int f = threadIdx.x; f < p.M * p.topk; f += blockDim.x) {
-    const int t = f / p.topk, e = s_id[f];
-    const int row = start[e] + __popc(tmask[e] & ((1u << t) - 1u));
-    s_token[row] = t;
-    if (blockIdx.x == 0) {
-      p.plan->row_token[row] = t;
-      p.plan->row_weight[row] = s_w[f];
-    }
-  }
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < groups; i += blockDim.x) {
-      p.plan->group_expert[i] = g_expert[i];
-      p.plan->group_row[i] = g_row[i];
-    }
-    if (threadIdx.x == 0) p.plan->groups = groups;
+  for (int f = threadIdx.x; f < p.M * p.topk; f += 32 * kMi8Warps) {
+    const int t = f / p.topk, e = r.id[f];
+    const int row = r.start[e] + __popc(r.tmask[e] & ((1u << t) - 1u));
+    r.row_token[row] = (uint16_t)t;
+    r.row_weight[row] = __uint_as_float(r.w[f]);
   }
   __syncthreads();
-
-  // ---- units: (group, 8 gate rows + 8 up rows) ----
-  const int tiles = p.F / 8;
-  const int units = groups * tiles;
-  const int g = lane >> 2, i4 = lane & 3;
-  const int pieces = (p.H + 63) / 64;                      // 64-wide pieces of K
-  const int pairs = (pieces + 1) / 2;                      // the warps take 128-byte pairs in turn
-  const int batches = (pairs + kMi8Warps1 * (kMi8Batch / 2) - 1) / (kMi8Warps1 * (kMi8Batch / 2));
-  uint4 au[kMi8Batch], av[kMi8Batch];
-  // k offset of this lane's 16 values of piece j of batch b
-  auto kof = [&](int b, int j) { return (((b * (kMi8Batch / 2) + (j >> 1)) * kMi8Warps1 + warp) * 2 + (j & 1)) * 64 + 16 * i4; };
-  auto rows_of = [&](int u) {
-    const int grp = u / tiles, f0 = (u % tiles) * 8;
-    return p.Wgu + ((int64_t)g_expert[grp] * 2 * p.F + f0 + g) * p.H;
-  };
-  auto load = [&](const int8_t* w, int b, int j) {
-    const int k = kof(b, j);
-    au[j] = k < p.H ? ldg_stream_u4(w + k) : zero4();
-    av[j] = k < p.H ? ldg_stream_u4(w + (int64_t)p.F * p.H + k) : zero4();
-  };
-  int u = blockIdx.x, buf = 0;
-  if (u < units) {
-    const int8_t* w = rows_of(u);
-#pragma unroll
-    for (int j = 0; j < kMi8Batch; ++j) load(w, 0, j);
-  }
-  for (; u < units; u += gridDim.x, buf ^= 1) {
-    const int grp = u / tiles, f0 = (u % tiles) * 8;
-    const int row0 = g_row[grp] & 0xFFFF, nrows = g_row[grp] >> 16, e = g_expert[grp];
-    const uint16_t* x = p.X + (int64_t)(g < nrows ? s_token[row0 + g] : 0) * p.H;
-    const int un = u + gridDim.x;
-    const int8_t* w_cur = rows_of(u);
-    const int8_t* w_next = un < units ? rows_of(un) : nullptr;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int b = 0; b < batches; ++b) {
-      const bool last = b + 1 == batches;
-#pragma unroll
-      for (int j = 0; j < kMi8Batch; ++j) {
-        const int k = kof(b, j);
-        uint4 bx[1][2];
-        const bool in = g < nrows && k < p.H;
-        bx[0][0] = in ? __ldg(reinterpret_cast<const uint4*>(x + k)) : zero4();
-        bx[0][1] = in ? __ldg(reinterpret_cast<const uint4*>(x + k + 8)) : zero4();
-        mi8_piece<1>(acc, au[j], av[j], bx);
-        if (!last)
-          load(w_cur, b + 1, j);
-        else if (w_next)
-          load(w_next, 0, j);
-      }
-    }
-    float(*r)[8] = red[buf][warp];
-    r[g][2 * i4] = acc[0];
-    r[g][2 * i4 + 1] = acc[1];
-    r[g + 8][2 * i4] = acc[2];
-    r[g + 8][2 * i4 + 1] = acc[3];
-    __syncthreads();
-    if (threadIdx.x < 64) {  // (f, row): 8 neighbouring threads write 8 neighbouring f
-      const int f = threadIdx.x & 7, c = threadIdx.x >> 3;
-      if (c < nrows) {
-        float gs = 0.f, us = 0.f;
-#pragma unroll
-        for (int wv = 0; wv < kMi8Warps1; ++wv) {
-          gs += red[buf][wv][f][c];
-          us += red[buf][wv][f + 8][c];
-        }
-        const float* s = p.sgu + (int64_t)e * 2 * p.F + f0 + f;
-        const float hv = silu_mul(gs * s[0], us * s[p.F]);
-        uint16_t* h = p.h + (int64_t)(row0 + c) * 3 * p.F + f0 + f;
-        float rest = hv;
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) {
-          // truncated, so that 3 x 8 bits hold all 24 of h and the first plane cannot overflow
-          const __nv_bfloat16 b = __float2bfloat16_rz(rest);
-          h[(int64_t)pl * p.F] = __bfloat16_as_ushort(b);
-          rest = isfinite(hv) ? rest - __bfloat162float(b) : 0.f;  // inf, NaN: the first plane alone
-        }
-      }
-    }
-  }
 }
 
-__global__ void __launch_bounds__(32 * kMi8Warps2, 1)
-mi8_down_kernel(Mi8Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ float sums[kMi8Warps2][kMi8MaxM][16 + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, i4 = lane & 3;
-  const int n0 = blockIdx.x * 16;
-  for (int i = lane; i < kMi8MaxM * 17; i += 32) (&sums[warp][0][0])[i] = 0.f;
-  __syncwarp();
-  const int groups = p.plan->groups;
-  const int pieces = (p.F + 63) / 64;
-  // items: (group, part of K); parts > 1 only when there are fewer groups than warps
-  const int parts = groups >= kMi8Warps2 ? 1 : max(1, min(kMi8Warps2 / max(groups, 1), pieces));
-  for (int it = warp; it < groups * parts; it += kMi8Warps2) {
-    const int grp = it / parts, part = it % parts;
-    const int e = p.plan->group_expert[grp], gr = p.plan->group_row[grp];
-    const int row0 = gr & 0xFFFF, nrows = gr >> 16;
-    const int c0 = pieces * part / parts, c1 = pieces * (part + 1) / parts;
-    const int8_t* w = p.Wd + ((int64_t)e * p.H + n0 + g) * p.F;
-    const uint16_t* h = p.h + (int64_t)(row0 + min(g, nrows - 1)) * 3 * p.F;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int cb = c0; cb < c1; cb += kMi8Batch) {
-      uint4 au[kMi8Batch], av[kMi8Batch];
-#pragma unroll
-      for (int j = 0; j < kMi8Batch; ++j) {
-        const int k = (cb + j) * 64 + 16 * i4;
-        const bool in = cb + j < c1 && k < p.F;
-        au[j] = in ? ldg_stream_u4(w + k) : zero4();
-        av[j] = in ? ldg_stream_u4(w + 8 * (int64_t)p.F + k) : zero4();
-      }
-#pragma unroll
-      for (int j = 0; j < kMi8Batch; ++j) {
-        if (cb + j >= c1) break;
-        const int k = (cb + j) * 64 + 16 * i4;
-        uint4 b[3][2];
-        const bool in = g < nrows && k < p.F;
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) {
-          b[pl][0] = in ? *reinterpret_cast<const uint4*>(h + (int64_t)pl * p.F + k) : zero4();
-          b[pl][1] = in ? *reinterpret_cast<const uint4*>(h + (int64_t)pl * p.F + k + 8) : zero4();
-        }
-        mi8_piece<3>(acc, au[j], av[j], b);
-      }
-    }
-    const float s0 = p.sd[(int64_t)e * p.H + n0 + g], s1 = p.sd[(int64_t)e * p.H + n0 + g + 8];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = 2 * i4 + c;
-      if (r < nrows) {
-        const int t = p.plan->row_token[row0 + r];
-        const float pw = p.plan->row_weight[row0 + r];
-        sums[warp][t][g] += pw * (s0 * acc[c]);
-        sums[warp][t][g + 8] += pw * (s1 * acc[2 + c]);
-      }
-    }
-    __syncwarp();
+// Scale of a row whose largest magnitude has these bits, and 1 / scale; a row of zeros: 0
+// and 0; a row with an infinity or a NaN: 0 and NaN, so that its products are NaN.
+// TWO: a power of two (0.25 .. 0.5 of the digits' range).
+template <bool TWO>
+__device__ __forceinline__ float2 mi8_scale(uint32_t bits) {
+  if (bits >= 0x7F800000u) return make_float2(0.f, __uint_as_float(0x7FC00000u));
+  if (bits == 0) return make_float2(0.f, 0.f);
+  if (TWO) {
+    // amax in [2^e, 2^(e+1)): S = 2^(21 - e), kept normal (below 2^-105 the digits lose range, no more)
+    const int e = max((int)(bits >> 23) - 127, -105);
+    const int s = min(21 - e, 126);
+    return make_float2(__uint_as_float((uint32_t)(127 + s) << 23), __uint_as_float((uint32_t)(127 - s) << 23));
   }
+  const float amax = fmaxf(__uint_as_float(bits), 0x1p-100f);
+  return make_float2(kMi8Top / amax, amax / kMi8Top);
+}
+
+// Digits of four values: byte i of word d is digit d (0 the highest) of value i.
+__device__ __forceinline__ void mi8_digits(const float (&x)[4], float S, uint32_t (&d)[3]) {
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int q = __float2int_rn(fminf(fmaxf(x[i] * S, -kMi8Top), kMi8Top));
+    v[i] = ((uint32_t)q + 0x00808080u) ^ 0x00808080u;  // bytes 2, 1, 0: the signed digits
+  }
+  const uint32_t a = __byte_perm(v[0], v[1], 0x5140), b = __byte_perm(v[2], v[3], 0x5140);  // digits 2, 1 of two values
+  d[2] = __byte_perm(a, b, 0x5410);
+  d[1] = __byte_perm(a, b, 0x7632);
+  d[0] = __byte_perm(__byte_perm(v[0], v[1], 0x0062), __byte_perm(v[2], v[3], 0x0062), 0x5410);
+}
+
+template <int PL, bool DOWN>
+__global__ void __launch_bounds__(32 * kMi8Warps)
+mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Mi8Route<PL> r;
+  __shared__ __align__(8) uint64_t bar_mem[3 * kMi8MaxStages + 4];
+  // scale and its inverse: kernel 1 of each token, kernel 2 of each row of h
+  __shared__ float2 s_scale[DOWN ? kMi8MaxRows : kMi8MaxM];
+  __shared__ uint32_t tmem_slot_mem;
+  __shared__ int abort_mem;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t stage_bytes = kI8ATile + (uint32_t)p.nb * kI8KB;
+  float* ysum = reinterpret_cast<float*>(smem + p.stages * stage_bytes);  // kernel 2: [M][128]
+  const uint32_t bars = smem_u32(bar_mem);
+  auto bar_a = [&](int s) { return bars + 8u * s; };                        // weights landed
+  auto bar_b = [&](int s) { return bars + 8u * (kMi8MaxStages + s); };      // digits written
+  auto bar_empty = [&](int s) { return bars + 8u * (2 * kMi8MaxStages + s); };
+  auto bar_tfull = [&](int a) { return bars + 8u * (3 * kMi8MaxStages + a); };
+  auto bar_tempty = [&](int a) { return bars + 8u * (3 * kMi8MaxStages + 2 + a); };
+  volatile int* abort_flag = &abort_mem;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(bar_a(s), 1);
+      mbar_init(bar_b(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar_tfull(a), 1);
+      mbar_init(bar_tempty(a), 4);
+    }
+    abort_mem = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot_mem)),
+                 "r"((uint32_t)p.tmem_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (DOWN)
+    for (int i = threadIdx.x; i < p.M * kI8Rows; i += blockDim.x) ysum[i] = 0.f;
+  // Kernel 1 reads its inputs after the kernel before it; kernel 2 starts once every CTA of
+  // kernel 1 has got past this wait, so the logits are complete for it already.
+  if (!DOWN) asm volatile("griddepcontrol.wait;" ::: "memory");
+  tc_fence_before();
+  mi8_route<PL>(p, r);  // (barriers within: the set-up above is visible after it)
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot_mem;
+  if (!DOWN) {
+    for (int t = warp; t < p.M; t += kMi8Warps) {
+      uint32_t m = 0;
+      for (int k = 8 * lane; k < p.H; k += 256) {
+        const uint4 x = ldg_u4(p.X + (int64_t)t * p.H + k);
+        m = __vmaxu2(__vmaxu2(m, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)),
+                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+      }
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+      if (lane == 0) s_scale[t] = mi8_scale<true>(m << 16);
+    }
+    __syncthreads();
+  }
+  if (!DOWN && blockIdx.x == 0)  // for kernel 2
+    for (int i = threadIdx.x; i < (p.H + kI8Rows - 1) / kI8Rows; i += blockDim.x) p.count[i] = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // this CTA's units: (group, tile of weight rows)
+  const int K = DOWN ? p.F : p.H;
+  const int nk = (K + kI8KB - 1) / kI8KB;
+  const int tiles = (p.F + 63) / 64;  // kernel 1
+  const int units = DOWN ? r.groups : r.groups * tiles;
+  const int first = DOWN ? (int)(blockIdx.x % (unsigned)p.split) : (int)blockIdx.x;
+  const int step = DOWN ? p.split : (int)gridDim.x;
+  const int col0 = DOWN ? (int)(blockIdx.x / (unsigned)p.split) * kI8Rows : 0;
+  auto group_of = [&](int u) { return DOWN ? u : u / tiles; };
+  // scale of row j of a group that starts at row0
+  auto row_scale = [&](int row0, int j) { return s_scale[DOWN ? row0 + j : r.row_token[row0 + j]]; };
+  auto columns = [&](int u) { return (4 * (r.group_row[group_of(u)] >> 16) + 15) / 16 * 16; };
+
+  const uint64_t limit = *const_cast<volatile unsigned long long*>(&g_wait_limit_ns);
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      const int drop = g_test_drop_stage;  // test hook; -1 in normal use
+      int it = 0;
+      I8Ring at;
+      bool ok = true;
+      for (int u = first; u < units && ok; u += step) {
+        const int e = r.group_expert[group_of(u)];
+        for (int k = 0; k < nk; ++k, ++it, at.next(p.stages)) {
+          const int s = at.s;
+          // (a barrier's phase before its first counts as complete)
+          if (!(ok = mbar_wait_l(bar_empty(s), at.parity ^ 1, abort_flag, limit))) break;
+          if (it == drop) continue;  // test hook: this stage never arrives
+          mbar_arrive_expect_tx(bar_a(s), kI8ATile);
+          const uint32_t a_dst = sbase + s * stage_bytes;
+          if (DOWN) {
+            tma_load_2d(a_dst, &tmap_w, k * kI8KB, e * p.H + col0, bar_a(s));
+          } else {
+            tma_load_gate_up(a_dst, &tmap_w, k * kI8KB, u % tiles * 4, e, bar_a(s));
+          }
+        }
+      }
+      if (*abort_flag)  // every issued copy lands before this CTA may exit
+        for (int i = max(0, it - p.stages); i < it; ++i)
+          if (i != drop) mbar_wait_drain(bar_a(i % p.stages), (i / p.stages) & 1);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      int done = 0;
+      I8Ring at;
+      bool ok = true;
+      for (int u = first; u < units && ok; u += step, ++done) {
+        const int a = done & 1;
+        if (done >= 2 && !(ok = mbar_wait_l(bar_tempty(a), (done / 2 - 1) & 1, abort_flag, limit))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(a * p.tstride);
+        const uint32_t idesc = i8_idesc(kI8Rows, columns(u));
+        for (int k = 0; k < nk; ++k, at.next(p.stages)) {
+          if (!(ok = mbar_wait_l(bar_b(at.s), at.parity, abort_flag, limit) &&
+                     mbar_wait_l(bar_a(at.s), at.parity, abort_flag, limit)))
+            break;
+          tc_fence_after();
+          const uint32_t a0 = sbase + at.s * stage_bytes;
+          const uint64_t ad = umma_desc_sw128(a0), bd = umma_desc_sw128(a0 + kI8ATile);
+#pragma unroll
+          for (int kk = 0; kk < kI8KB / 32; ++kk)  // 32 bytes of K on: 2 in the descriptors' units
+            umma_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
+          umma_commit(bar_empty(at.s));
+        }
+        if (ok) umma_commit(bar_tfull(a));
+      }
+    }
+  } else if (warp < 6) {
+    // ---------------- epilogue ----------------
+    const int q = warp & 3;
+    int done = 0;
+    for (int u = first; u < units; u += step, ++done) {
+      const int a = done & 1;
+      const int e = r.group_expert[group_of(u)], gr = r.group_row[group_of(u)];
+      const int row0 = gr & 0xFFFF, rows = gr >> 16;
+      const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * p.tstride);
+      const int tile = DOWN ? 0 : u % tiles;
+      bool up = lane >= 16;
+      const int f = tile * 64 + 16 * q + (lane & 15);  // kernel 1
+      const int n = col0 + 32 * q + lane;              // kernel 2
+      float w = 0.f;
+      if (DOWN) {
+        if (n < p.H) w = p.sd[(int64_t)e * p.H + n];
+      } else if (f < p.F) {
+        w = p.sgu[(int64_t)e * 2 * p.F + (up ? p.F : 0) + f];
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait_l(bar_tfull(a), (done / 2) & 1, abort_flag, limit))) break;
+      tc_fence_after();
+      const float inv = lane < rows ? row_scale(row0, lane).y : 0.f;  // (written before the digits)
+      for (int j = 0; j < rows; j += 4) {
+        int32_t v[16];
+        tmem_ld16(d + 4 * j, v);
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float back = __shfl_sync(0xffffffffu, inv, min(j + i, rows - 1));
+          y[i] = fmaf((float)v[4 * i], 65536.f, fmaf((float)v[4 * i + 1], 256.f, (float)v[4 * i + 2])) * back * w;
+        }
+        if (DOWN) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (j + i < rows) ysum[r.row_token[row0 + j + i] * kI8Rows + 32 * q + lane] += r.row_weight[row0 + j + i] * y[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, up ? y[i] : y[i + 1], 16);
+            const float hv = up ? silu_mul(got, y[i + 1]) : silu_mul(y[i], got);
+            const int rj = j + i + (up ? 1 : 0);
+            const bool in = rj < rows && f < p.F;
+            uint32_t m = in ? __float_as_uint(hv) & 0x7FFFFFFFu : 0u;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (in) p.h[(int64_t)(row0 + rj) * p.F + f] = hv;
+            if (rj < rows && (lane & 15) == 0) p.hmax[(int64_t)(row0 + rj) * p.hparts + tile * 4 + q] = m;
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_tempty(a));
+    }
+  } else {
+    // ---------------- digits ----------------
+    const int me = warp - 6;
+    if (DOWN) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // h is kernel 1's
+      for (int row = threadIdx.x - 6 * 32; row < p.M * p.topk; row += 32 * kMi8DigitWarps) {
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int i = 0; i < p.hparts; i += 4) {
+          const uint4 h = __ldcg(reinterpret_cast<const uint4*>(p.hmax + (int64_t)row * p.hparts + i));
+          m = max(max(m, max(h.x, h.y)), max(h.z, h.w));
+        }
+        s_scale[row] = mi8_scale<false>(m);
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kMi8DigitWarps) : "memory");
+    }
+    int turn = 0;  // whose stage it is
+    I8Ring ring;
+    bool ok = true;
+    for (int u = first; u < units && ok; u += step) {
+      const int gr = r.group_row[group_of(u)], row0 = gr & 0xFFFF, rows = gr >> 16;
+      const float scale = lane < rows ? row_scale(row0, lane).x : 0.f;  // lane j: row j's
+      for (int k = 0; k < nk; ++k, turn = (turn + 1) % kMi8DigitWarps, ring.next(p.stages)) {
+        if (turn != me) continue;
+        const int s = ring.s;
+        // (parity tells passes apart as long as a warp is never two passes ahead of the
+        // MMAs: with at least kMi8DigitWarps stages, its last stage came after them)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait_l(bar_empty(s), ring.parity ^ 1, abort_flag, limit)))) break;
+        uint8_t* b = smem + s * stage_bytes + kI8ATile;
+        const int at = k * kI8KB + 4 * lane;
+        for (int j0 = 0; j0 < rows; j0 += 4) {
+          float x[4][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = row0 + min(j0 + j, rows - 1);
+            if (DOWN) {
+              const float4 t = at < K ? __ldcg(reinterpret_cast<const float4*>(p.h + (int64_t)row * p.F + at))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+              x[j][0] = t.x, x[j][1] = t.y, x[j][2] = t.z, x[j][3] = t.w;
+            } else {
+              const uint2 t = at < K ? __ldg(reinterpret_cast<const uint2*>(p.X + (int64_t)r.row_token[row] * p.H + at))
+                                     : make_uint2(0u, 0u);
+              x[j][0] = __uint_as_float(t.x << 16), x[j][1] = __uint_as_float(t.x & 0xFFFF0000u);
+              x[j][2] = __uint_as_float(t.y << 16), x[j][3] = __uint_as_float(t.y & 0xFFFF0000u);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float S = __shfl_sync(0xffffffffu, scale, min(j0 + j, rows - 1));
+            if (j0 + j < rows) {
+              uint32_t dg[3];
+              mi8_digits(x[j], S, dg);
+#pragma unroll
+              for (int c = 0; c < 3; ++c)
+                *reinterpret_cast<uint32_t*>(b + sw128_offset(4 * (j0 + j) + c, lane >> 2) + 4 * (lane & 3)) = dg[c];
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_b(s));
+      }
+    }
+  }
+
+  // ---- teardown; kernel 2 first sums over the cluster ----
+  tc_fence_before();
   __syncthreads();
-  for (int i = threadIdx.x; i < p.M * 16; i += blockDim.x) {
-    const int t = i >> 4, n = i & 15;
-    float y = 0.f;
-    for (int wv = 0; wv < kMi8Warps2; ++wv) y += sums[wv][t][n];
-    const int64_t at = (int64_t)t * p.H + n0 + n;
-    p.Y[at] = p.residual ? p.residual[at] + y : y;
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)p.tmem_cols)
+                 : "memory");
+  }
+  if constexpr (DOWN) {
+    // The last CTA of a column tile to arrive adds the splits' sums, in their order.
+    __shared__ int s_last;
+    const int tile = col0 / kI8Rows, n = p.M * kI8Rows;
+    if (p.split > 1) {
+      float* mine = p.part + ((int64_t)tile * p.split + first) * n;
+      for (int i = 4 * threadIdx.x; i < n; i += 4 * blockDim.x)
+        __stcg(reinterpret_cast<float4*>(mine + i), *reinterpret_cast<const float4*>(ysum + i));
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) s_last = atomicAdd(p.count + tile, 1) == p.split - 1;
+      __syncthreads();
+      if (!s_last) return;
+      __threadfence();
+    }
+    for (int i = 4 * threadIdx.x; i < n; i += 4 * blockDim.x) {
+      const int t = i / kI8Rows, c = col0 + i % kI8Rows;
+      if (c >= p.H) continue;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.split == 1) {
+        y = *reinterpret_cast<const float4*>(ysum + i);
+      } else {
+#pragma unroll 4
+        for (int q = 0; q < p.split; ++q) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + ((int64_t)tile * p.split + q) * n + i));
+          y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+        }
+      }
+      const int64_t at = (int64_t)t * p.H + c;  // (H % 16 == 0: four columns are in or out together)
+      if (p.residual) {
+        const float4 v = *reinterpret_cast<const float4*>(p.residual + at);
+        y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+      }
+      *reinterpret_cast<float4*>(p.Y + at) = y;
+    }
   }
 }
 

@@ -59,10 +59,11 @@ q4k_status launch_status(cudaError_t e) {
 // start while that kernel finishes; every such kernel here executes
 // griddepcontrol.wait before it reads anything the previous kernel writes.
 template <typename... KArgs, typename... Args>
-q4k_status launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+q4k_status launch_pdl_smem(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -70,6 +71,11 @@ q4k_status launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, cudaStream_t s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return launch_status(cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...));
+}
+
+template <typename... KArgs, typename... Args>
+q4k_status launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+  return launch_pdl_smem(k, grid, block, 0, s, args...);
 }
 
 // ---------------------------------------------------------------- GEMV ----
@@ -506,7 +512,8 @@ q4k_status i8_gemm_t(const int8_t* W, const int8_t* X, I8GemmParams p, cudaStrea
   p.tmem_cols = 32;
   while (p.tmem_cols < (c > 1 ? 1 : 2) * p.tstride) p.tmem_cols *= 2;
   CUtensorMap tw, tx;
-  if (!make_tmap_i8(&tw, W, p.N, p.K, SWIGLU ? 16 : kI8Rows) || !make_tmap_i8(&tx, X, p.M, p.K, p.nt))
+  p.boxed = SWIGLU && rows % 16 == 0;
+  if (!(p.boxed ? make_tmap_gate_up(&tw, W, 1, rows, p.K) : make_tmap_i8(&tw, W, p.N, p.K, SWIGLU ? 16 : kI8Rows)) || !make_tmap_i8(&tx, X, p.M, p.K, p.nt))
     return Q4K_ERR_CUDA;
   static std::atomic<size_t> smem_set[2][kMaxDevices];
   if (c > 1)
@@ -515,23 +522,40 @@ q4k_status i8_gemm_t(const int8_t* W, const int8_t* X, I8GemmParams p, cudaStrea
                    smem_set[0], s);
 }
 
-template <int PL>
-q4k_status launch_mi8(const Mi8Params& p, cudaStream_t s) {
-  auto* k = mi8_gate_up_kernel<PL>;
-  static std::atomic<int> per_sm[kMaxDevices];
-  const int dev = current_device();
-  if (dev < 0 || dev >= kMaxDevices || sm_count() <= 0) return Q4K_ERR_CUDA;
-  int n = per_sm[dev].load();
-  if (n <= 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, 32 * kMi8Warps1, 0) != cudaSuccess || n <= 0)
-      return launch_status(cudaErrorUnknown);
-    per_sm[dev].store(n);
+// Shared memory of the layer's kernels: for few tokens half of an SM's, so that a CTA of
+// kernel 2 finds room beside one of kernel 1; else all of it.
+template <int PL, bool DOWN>
+q4k_status launch_mi8_t(const CUtensorMap& tw, Mi8Params p, int grid, cudaStream_t s) {
+  auto* k = mi8_kernel<PL, DOWN>;
+  static std::atomic<size_t> smem_set[kMaxDevices];
+  constexpr size_t fixed = sizeof(Mi8Route<PL>) + 512 + (DOWN ? kMi8MaxRows : kMi8MaxM) * sizeof(float2);  // static arrays
+  const size_t stage = kI8ATile + (size_t)p.nb * kI8KB, ysum = DOWN ? (size_t)p.M * kI8Rows * sizeof(float) : 0;
+  size_t smem = 0;
+  for (size_t budget : {kGemvTwoPerSm, (size_t)232448}) {
+    smem = budget - fixed;
+    p.stages = std::min<int>(kMi8MaxStages, (int)((smem - 1024 - ysum) / stage));
+    if (p.M <= 8 && p.stages >= kMi8DigitWarps) break;
   }
-  const int64_t most = (int64_t)p.M * p.topk * (p.F / 8);  // units, were every group one row
-  const q4k_status st = launch_pdl(k, dim3((unsigned)std::min<int64_t>(most, (int64_t)n * sm_count())),
-                                   dim3(32 * kMi8Warps1), s, p);
+  if (p.stages < kMi8DigitWarps) return Q4K_ERR_UNSUPPORTED;  // (does not happen: M <= 32)
+  if (ensure_smem(k, 232448 - fixed, smem_set) != cudaSuccess) return launch_status(cudaErrorUnknown);
+  return launch_pdl_smem(k, dim3((unsigned)grid), dim3(32 * kMi8Warps), smem, s, tw, p);
+}
+
+// CTAs per column tile of kernel 2: as many as keep one CTA per SM, at most one per expert.
+int mi8_split(int M, int E, int topk, int H) {
+  const int tiles = (H + kI8Rows - 1) / kI8Rows;
+  return std::max(1, std::min({std::min(sm_count(), kMi8MaxCtas) / tiles, E, M * topk}));
+}
+
+template <int PL>
+q4k_status launch_mi8(Mi8Params p, const int8_t* Wgu, const int8_t* Wd, cudaStream_t s) {
+  CUtensorMap tgu, td;
+  if (!make_tmap_gate_up(&tgu, Wgu, p.E, p.F, p.H) || !make_tmap_i8(&td, Wd, (int64_t)p.E * p.H, p.F, kI8Rows))
+    return Q4K_ERR_CUDA;
+  const int64_t most = (int64_t)std::min(p.E, p.M * p.topk) * mi8_tiles(p.F);  // units of kernel 1 at most
+  const q4k_status st = launch_mi8_t<PL, false>(tgu, p, (int)std::min<int64_t>(most, sm_count()), s);
   if (st != Q4K_OK) return st;
-  return launch_pdl(mi8_down_kernel, dim3((unsigned)(p.H / 16)), dim3(32 * kMi8Warps2), s, p);
+  return launch_mi8_t<PL, true>(td, p, (p.H + kI8Rows - 1) / kI8Rows * p.split, s);
 }
 
 }  // namespace
@@ -816,8 +840,10 @@ q4k_status moe_i8_layer(const float* logits, int M, int E, int topk, const int8_
                         const float* residual, float* Y, void* ws, size_t ws_bytes, void* stream) {
   if (M < 0 || E <= 0 || topk <= 0 || H <= 0 || F <= 0 || H % 16 || F % 16) return Q4K_ERR_SHAPE;
   if (M > kMi8MaxM || E > kMaxE || topk > kMaxTopk || topk > E) return Q4K_ERR_UNSUPPORTED;
-  if (F > 0x7fffffff / (kMi8MaxRows / 8)) return Q4K_ERR_UNSUPPORTED;  // units in 32 bits
+  // the sums fit int32, the rows of the weights and the units 32 bits
+  if (H > kI8MaxK || F > kI8MaxK || (int64_t)E * std::max(2 * F, H) > 0x7fffffffLL - 256) return Q4K_ERR_UNSUPPORTED;
   if (M == 0) return Q4K_OK;
+  if (sm_count() <= 0) return Q4K_ERR_CUDA;
   if (!logits || !W_gate_up || !s_gate_up || !W_down || !s_down || !X || !Y || !ws) return Q4K_ERR_NULL;
   if (!aligned16(logits) || !aligned16(W_gate_up) || !aligned16(s_gate_up) || !aligned16(W_down) ||
       !aligned16(s_down) || !aligned16(X) || !aligned16(Y) || !aligned16(ws) || (residual && !aligned16(residual)))
@@ -825,31 +851,37 @@ q4k_status moe_i8_layer(const float* logits, int M, int E, int topk, const int8_
   if (ws_bytes < q4k_workspace_bytes(Q4K_OP_MOE_I8, M, H, F, E, topk)) return Q4K_ERR_WORKSPACE;
   Mi8Params p = {};
   p.logits = logits;
-  p.Wgu = W_gate_up;
   p.sgu = s_gate_up;
-  p.Wd = W_down;
   p.sd = s_down;
   p.X = X;
   p.residual = residual;
   p.Y = Y;
-  p.plan = static_cast<Mi8Plan*>(ws);
-  p.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + (mi8_ws_bytes(0, 0, 0)));
+  p.hparts = 4 * mi8_tiles(F);
+  p.h = static_cast<float*>(ws);
+  uint8_t* w = static_cast<uint8_t*>(ws) + mi8_ws_h(M, topk, F);
+  p.hmax = reinterpret_cast<uint32_t*>(w);
+  p.count = reinterpret_cast<int32_t*>(w += mi8_ws_hmax(M, topk, F));
+  p.part = reinterpret_cast<float*>(w + ((H + kI8Rows - 1) / kI8Rows + 3) / 4 * 16);
+  p.split = mi8_split(M, E, topk, H);
   p.M = M;
   p.E = E;
   p.topk = topk;
   p.H = H;
   p.F = F;
+  p.nb = (4 * M + 15) / 16 * 16;
+  p.tstride = (p.nb + 31) / 32 * 32;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < 2 * p.tstride) p.tmem_cols *= 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (E <= 128) return launch_mi8<4>(p, s);
-  if (E <= 256) return launch_mi8<8>(p, s);
-  return launch_mi8<32>(p, s);
+  if (E <= 128) return launch_mi8<4>(p, W_gate_up, W_down, s);
+  if (E <= 256) return launch_mi8<8>(p, W_gate_up, W_down, s);
+  return launch_mi8<32>(p, W_gate_up, W_down, s);
 }
 
 size_t q4k_workspace_bytes(int op, int M, int N, int K, int E, int topk) {
-  (void)N;
   if (op == Q4K_OP_MOE_I8) {
-    if (M <= 0 || K <= 0 || topk <= 0) return 0;
-    return mi8_ws_bytes(M, topk, K);
+    if (M <= 0 || N <= 0 || K <= 0 || topk <= 0) return 0;
+    return mi8_ws_bytes(M, topk, N, K);
   }
   if (op == Q4K_OP_ROUTE) {
     if (M <= 0 || E <= 0) return 0;

@@ -305,7 +305,10 @@ def test_moe_nan_logits_rank_last():
     assert torch.equal(Y, q.moe_i8_layer(clean, 4, Wg, sg, Wd, sd, X))
     L[1] = float("nan")  # nothing left to rank: this token alone is NaN
     Y2 = q.moe_i8_layer(L, 4, Wg, sg, Wd, sd, X)
-    assert torch.isnan(Y2[1]).all() and torch.equal(Y2[[0, 2]], Y[[0, 2]])
+    assert torch.isnan(Y2[1]).all()
+    # the others' sums are taken in an order that depends on the whole routing: equal to fp32
+    # rounding, not bit for bit
+    check_moe(Y2[[0, 2]], L[[0, 2]], 4, Wg, sg, Wd, sd, X[[0, 2]])
 
 
 def test_moe_non_finite_token_stays_alone():
