@@ -46,6 +46,8 @@ constexpr int kMi8MaxM = 32;
 constexpr int kMi8MaxRows = kMi8MaxM * kMaxTopk;  // (token, slot) pairs
 constexpr int kMi8Warps = 10;
 constexpr int kMi8DigitWarps = 4;
+constexpr int kMi8Cluster = 4;    // CTAs that share the routing
+constexpr int kMi8GroupRows = 8;  // rows of a group at most
 constexpr int kMi8MaxStages = 10;
 constexpr float kMi8Top = 8355711.f;  // 127 * 65536 + 127 * 256 + 127: the largest three digits hold
 
@@ -62,7 +64,7 @@ struct Mi8Params {
   int32_t* count;  // kernel 2: [column tile], splits that have arrived
   int M, E, topk, H, F;
   int hparts;  // 4 per tile of kernel 1
-  int nb;      // columns that a stage has room for: 4 M rounded up to 16
+  int nb;      // columns that a stage has room for: 4 per row of a group, rounded up to 16
   int stages, tstride, tmem_cols;
   int split;   // kernel 2: CTAs that share a column tile, taking the experts in turn
 };
@@ -83,144 +85,49 @@ inline size_t mi8_ws_bytes(int M, int topk, int H, int F) {
 // Order of the logits as unsigned keys: -inf .. +inf, a NaN below them all, 0 for none.
 __device__ __forceinline__ uint32_t mi8_key(float v) { return v != v ? 1u : order_key(v); }
 
-// Top-k of one token by a whole warp from its PL logits per lane (expert 32 i + lane), as
-// keys: the j-th expert (higher logit first, equal logits by the lower id) goes to out[j],
-// its key to keys[j] (shared memory). Each lane keeps its keys sorted, so that a round is
-// one reduction, one ballot and a shift in the winning lane.
+// Top-k of one token by a whole warp, from PL logits per lane (expert 32 i + lane) as keys:
+// the j-th expert (higher logit first, equal logits by the lower id) goes to id[j], its key
+// to keys[j]. Ranks are counted, not found round by round (a round of warp-wide reductions
+// measured ~380 cycles): the topk-th largest of the 32 lanes' own maxima bounds the topk-th
+// key of all from below, the few keys that reach it are collected, and each of them counts
+// those before it. list: room for 32 PL entries of this warp's own, 16-byte aligned.
 template <int PL>
-__device__ __forceinline__ void mi8_topk(uint32_t (&key)[PL], int topk, int lane, uint16_t* out, uint32_t* keys) {
-  int idx[PL];
+__device__ __forceinline__ void mi8_topk(const uint32_t (&key)[PL], int topk, int lane, uint64_t* list, uint16_t* id,
+                                         uint32_t* keys) {
+  uint32_t m = key[0];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) idx[i] = 32 * i + lane;
-  if constexpr (PL <= 8) {
+  for (int i = 1; i < PL; ++i) m = max(m, key[i]);
+  // distinct, and off by less than the 5 bits that the bound gives away below
+  m = (m & ~31u) | (31u - lane);
+  uint32_t* maxima = reinterpret_cast<uint32_t*>(list);
+  maxima[lane] = m;
+  __syncwarp();
+  int rank = 0;
 #pragma unroll
-    for (int i = 1; i < PL; ++i)  // insertion: equal keys stay in order of id
-#pragma unroll
-      for (int j = i; j > 0; --j) {
-        const bool sw = key[j] > key[j - 1];
-        const uint32_t a = sw ? key[j] : key[j - 1], b = sw ? key[j - 1] : key[j];
-        const int c = sw ? idx[j] : idx[j - 1], d = sw ? idx[j - 1] : idx[j];
-        key[j - 1] = a, key[j] = b, idx[j - 1] = c, idx[j] = d;
-      }
+  for (int j = 0; j < 8; ++j) {
+    const uint4 o = reinterpret_cast<const uint4*>(maxima)[j];
+    rank += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
   }
-  for (int k = 0; k < topk; ++k) {
-    uint32_t best = key[0];
-    int bi = idx[0];
-    if constexpr (PL > 8) {
+  const uint32_t bound = __shfl_sync(0xffffffffu, m, __ffs(__ballot_sync(0xffffffffu, rank == topk - 1)) - 1) & ~31u;
+  int count = 0;
 #pragma unroll
-      for (int i = 1; i < PL; ++i)
-        if (key[i] > best) {
-          best = key[i];
-          bi = idx[i];
-        }
-    }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const unsigned who = __ballot_sync(0xffffffffu, best == top);
-    bool mine = best == top;
-    if (who & (who - 1)) {  // (the same for all lanes)
-      const uint32_t lowest = __reduce_min_sync(0xffffffffu, mine ? (uint32_t)bi : 0xffffffffu);
-      mine = (uint32_t)bi == lowest;
-    }
-    if (mine) {
-      out[k] = (uint16_t)bi;
-      keys[k] = top;
-      if constexpr (PL <= 8) {
-#pragma unroll
-        for (int i = 0; i + 1 < PL; ++i) {
-          key[i] = key[i + 1];
-          idx[i] = idx[i + 1];
-        }
-        key[PL - 1] = 0;
-      } else {
-#pragma unroll
-        for (int i = 0; i < PL; ++i)
-          if (idx[i] == bi) key[i] = 0;
-      }
+  for (int i = 0; i < PL; ++i) {
+    const bool in = key[i] != 0 && key[i] >= bound;
+    const unsigned who = __ballot_sync(0xffffffffu, in);  // (also: every lane has read the maxima)
+    if (in) list[count + __popc(who & ((1u << lane) - 1u))] = (uint64_t)key[i] << 32 | (0xffffffffu - (32 * i + lane));
+    count += __popc(who);
+  }
+  __syncwarp();
+  for (int c = lane; c < count; c += 32) {
+    const uint64_t mine = list[c];
+    int before = 0;
+    for (int j = 0; j < count; ++j) before += list[j] > mine;
+    if (before < topk) {
+      id[before] = (uint16_t)(0xffffffffu - (uint32_t)mine);
+      keys[before] = (uint32_t)(mine >> 32);
     }
   }
-}
-
-// The routing of all tokens, as every CTA of both kernels holds it: rows sorted by
-// (expert, token), the rows of one expert forming a group.
-template <int PL>
-struct Mi8Route {
-  unsigned tmask[32 * PL];  // tokens that selected expert e
-  int start[32 * PL];       // e's first row
-  uint16_t id[kMi8MaxRows];  // [token][slot]
-  uint32_t w[kMi8MaxRows];   // the logits' keys, then the weights' bits
-  uint16_t group_expert[kMi8MaxRows];
-  int group_row[kMi8MaxRows];  // first row | number of rows << 16
-  uint16_t row_token[kMi8MaxRows];
-  float row_weight[kMi8MaxRows];
-  int groups;
-};
-
-template <int PL>
-__device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e < 32 * PL; e += 32 * kMi8Warps) r.tmask[e] = 0u;
-  __syncthreads();
-  uint32_t next[PL];
-  auto load = [&](int t) {
-    const float* row = p.logits + (int64_t)t * p.E;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) next[i] = t < p.M && 32 * i + lane < p.E ? mi8_key(row[32 * i + lane]) : 0u;
-  };
-  load(warp);
-#pragma unroll 1
-  for (int t = warp; t < p.M; t += kMi8Warps) {
-    uint32_t key[PL];
-#pragma unroll
-    for (int i = 0; i < PL; ++i) key[i] = next[i];
-    load(t + kMi8Warps);  // under this token's rounds
-    uint16_t* id = r.id + t * p.topk;
-    uint32_t* w = r.w + t * p.topk;
-    mi8_topk<PL>(key, p.topk, lane, id, w);
-    __syncwarp();
-    // softmax over the selected: lane j has the j-th, the sum in a fixed butterfly order
-    const uint32_t k = w[min(lane, p.topk - 1)], k0 = w[0];
-    const float nan = __uint_as_float(0x7FC00000u);
-    const float v = k == 1u ? nan : key_value(k), v0 = k0 == 1u ? nan : key_value(k0);
-    const float ek = lane < p.topk ? expf(v - v0) : 0.f;
-    float den = ek;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    if (lane < p.topk) {
-      w[lane] = __float_as_uint(ek / den);
-      atomicOr(&r.tmask[id[lane]], 1u << t);
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int rows = 0, groups = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int c = __popc(r.tmask[e0 + lane]);
-      int sum = c;  // inclusive scan
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += a;
-      }
-      const unsigned some = __ballot_sync(0xffffffffu, c > 0);
-      r.start[e0 + lane] = rows + sum - c;
-      if (c > 0) {
-        const int grp = groups + __popc(some & ((1u << lane) - 1u));
-        r.group_expert[grp] = (uint16_t)(e0 + lane);
-        r.group_row[grp] = (rows + sum - c) | c << 16;
-      }
-      rows += __shfl_sync(0xffffffffu, sum, 31);
-      groups += __popc(some);
-    }
-    if (lane == 0) r.groups = groups;
-  }
-  __syncthreads();
-  for (int f = threadIdx.x; f < p.M * p.topk; f += 32 * kMi8Warps) {
-    const int t = f / p.topk, e = r.id[f];
-    const int row = r.start[e] + __popc(r.tmask[e] & ((1u << t) - 1u));
-    r.row_token[row] = (uint16_t)t;
-    r.row_weight[row] = __uint_as_float(r.w[f]);
-  }
-  __syncthreads();
+  __syncwarp();
 }
 
 // Scale of a row whose largest magnitude has these bits, and 1 / scale; a row of zeros: 0
@@ -238,6 +145,131 @@ __device__ __forceinline__ float2 mi8_scale(uint32_t bits) {
   }
   const float amax = fmaxf(__uint_as_float(bits), 0x1p-100f);
   return make_float2(kMi8Top / amax, amax / kMi8Top);
+}
+
+// The routing of all tokens, as every CTA of both kernels holds it: rows sorted by
+// (expert, token), cut into groups of up to kMi8GroupRows rows of one expert.
+template <int PL>
+struct Mi8Route {
+  unsigned tmask[32 * PL];   // tokens that selected expert e
+  uint16_t start[32 * PL];   // e's first row
+  uint16_t id[kMi8MaxRows];  // [token][slot]
+  uint32_t w[kMi8MaxRows];   // the logits' keys, then the weights' bits
+  uint16_t group_expert[kMi8MaxRows];
+  int group_row[kMi8MaxRows];  // first row | number of rows << 16
+  uint16_t row_token[kMi8MaxRows];
+  float row_weight[kMi8MaxRows];
+  int groups;
+};
+
+// Stores to, and an OR into, the variable at this place in the shared memory of CTA `rank`
+// of the cluster.
+__device__ __forceinline__ uint32_t map_cluster(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void st_cluster(uint32_t* p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_cluster(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint16_t* p, uint32_t rank, uint16_t v) {
+  asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(map_cluster(p, rank)), "h"(v) : "memory");
+}
+__device__ __forceinline__ void or_cluster(unsigned* p, uint32_t rank, unsigned v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.or.b32 %0, [%1], %2;" : "=r"(old) : "r"(map_cluster(p, rank)), "r"(v) : "memory");
+}
+
+// Every CTA needs the whole routing, but were every CTA to read all logits (and, for their
+// scales, all of X), 148 SMs would ask a few L2 slices for the same lines: 6 us for 32
+// tokens of 128 experts, and as much for X. So the CTAs of a cluster route a share of the
+// tokens each, a warp per token, and write what they find into each other's shared memory.
+// SCALES: also the tokens' scales into `scale`. scratch: 32 PL entries of 8 bytes per warp.
+// The masks are cleared, and that is known to the whole cluster, before.
+template <int PL, bool SCALES>
+__device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r, float2* scale, uint8_t* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = (int)(blockIdx.x % kMi8Cluster);
+  uint64_t* list = reinterpret_cast<uint64_t*>(scratch) + warp * 32 * PL;
+#pragma unroll 1
+  for (int t = rank + kMi8Cluster * warp; t < p.M; t += kMi8Cluster * kMi8Warps) {
+    float logit[PL];
+#pragma unroll
+    for (int j = 0; j < PL; ++j) logit[j] = 32 * j + lane < p.E ? p.logits[(int64_t)t * p.E + 32 * j + lane] : 0.f;
+    if (SCALES) {
+      uint32_t m = 0;
+#pragma unroll 8
+      for (int k = 8 * lane; k < p.H; k += 256) {
+        const uint4 x = ldg_u4(p.X + (int64_t)t * p.H + k);
+        m = __vmaxu2(__vmaxu2(m, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)),
+                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+      }
+      const float2 sc = mi8_scale<true>(__reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)) << 16);
+      if (lane < kMi8Cluster) {
+        st_cluster(reinterpret_cast<uint32_t*>(&scale[t].x), lane, __float_as_uint(sc.x));
+        st_cluster(reinterpret_cast<uint32_t*>(&scale[t].y), lane, __float_as_uint(sc.y));
+      }
+    }
+    uint32_t key[PL];
+#pragma unroll
+    for (int j = 0; j < PL; ++j) key[j] = 32 * j + lane < p.E ? mi8_key(logit[j]) : 0u;
+    uint16_t* id = r.id + t * p.topk;
+    uint32_t* w = r.w + t * p.topk;
+    mi8_topk<PL>(key, p.topk, lane, list, id, w);
+    // softmax over the selected: lane j has the j-th, the sum in a fixed butterfly order
+    const uint32_t k = w[min(lane, p.topk - 1)], k0 = w[0];
+    const float nan = __uint_as_float(0x7FC00000u);
+    const float v = k == 1u ? nan : key_value(k), v0 = k0 == 1u ? nan : key_value(k0);
+    const float ek = lane < p.topk ? expf(v - v0) : 0.f;
+    float den = ek;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if (lane < p.topk) {
+      const uint16_t e = id[lane];
+#pragma unroll
+      for (int c = 0; c < kMi8Cluster; ++c) {
+        st_cluster(id + lane, c, e);
+        st_cluster(w + lane, c, __float_as_uint(ek / den));
+        or_cluster(&r.tmask[e], c, 1u << t);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_barrier();
+  // rows and groups: a thread per expert, each warp 32 of them
+  for (int e0 = 32 * warp; e0 < 32 * PL; e0 += 32 * kMi8Warps) {
+    // those of the experts before e0, counted anew by each warp
+    int c0 = 0;
+    for (int e = lane; e < e0; e += 32) {
+      const int c = __popc(r.tmask[e]);
+      c0 += c | (c + kMi8GroupRows - 1) / kMi8GroupRows << 16;
+    }
+    c0 = (int)__reduce_add_sync(0xffffffffu, (unsigned)c0);
+    const int c = __popc(r.tmask[e0 + lane]), n = (c + kMi8GroupRows - 1) / kMi8GroupRows;
+    int sum = c | n << 16;  // inclusive scan of both
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += a;
+    }
+    sum += c0;
+    const int row = (sum & 0xFFFF) - c, grp = (sum >> 16) - n;
+    r.start[e0 + lane] = (uint16_t)row;
+    for (int i = 0; i < n; ++i) {
+      r.group_expert[grp + i] = (uint16_t)(e0 + lane);
+      r.group_row[grp + i] = (row + kMi8GroupRows * i) | min(kMi8GroupRows, c - kMi8GroupRows * i) << 16;
+    }
+    if (e0 == 32 * PL - 32 && lane == 31) r.groups = grp + n;
+  }
+  __syncthreads();
+  for (int f = threadIdx.x; f < p.M * p.topk; f += 32 * kMi8Warps) {
+    const int t = f / p.topk, e = r.id[f];
+    const int at = r.start[e] + __popc(r.tmask[e] & ((1u << t) - 1u));
+    r.row_token[at] = (uint16_t)t;
+    r.row_weight[at] = __uint_as_float(r.w[f]);
+  }
+  fence_async_smem();  // the scratch becomes stages of bulk copies
+  __syncthreads();
 }
 
 // Digits of four values: byte i of word d is digit d (0 the highest) of value i.
@@ -296,28 +328,26 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (DOWN)
-    for (int i = threadIdx.x; i < p.M * kI8Rows; i += blockDim.x) ysum[i] = 0.f;
   // Kernel 1 reads its inputs after the kernel before it; kernel 2 starts once every CTA of
   // kernel 1 has got past this wait, so the logits are complete for it already.
+  for (int e = threadIdx.x; e < 32 * PL; e += blockDim.x) r.tmask[e] = 0u;
+  if (!DOWN) {
+    // this warp's tokens into L2 (a prefetch may precede the wait: it returns nothing, and L2
+    // is where the kernel before this one writes)
+    for (int t = (int)(blockIdx.x % kMi8Cluster) + kMi8Cluster * warp; t < p.M; t += kMi8Cluster * kMi8Warps)
+      for (int i = 32 * lane; i < p.E; i += 32 * 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.logits + (int64_t)t * p.E + i));
+    for (int t = (int)(blockIdx.x % kMi8Cluster) + kMi8Cluster * warp; t < p.M; t += kMi8Cluster * kMi8Warps)
+      for (int i = 64 * lane; i < p.H; i += 64 * 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.X + (int64_t)t * p.H + i));
+  }
+  __syncwarp();
+  cluster_barrier();  // the masks are clear in the whole cluster
   if (!DOWN) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
-  mi8_route<PL>(p, r);  // (barriers within: the set-up above is visible after it)
+  mi8_route<PL, !DOWN>(p, r, s_scale, smem);  // (barriers within: the set-up above is visible after it)
   tc_fence_after();
   const uint32_t tmem = tmem_slot_mem;
-  if (!DOWN) {
-    for (int t = warp; t < p.M; t += kMi8Warps) {
-      uint32_t m = 0;
-      for (int k = 8 * lane; k < p.H; k += 256) {
-        const uint4 x = ldg_u4(p.X + (int64_t)t * p.H + k);
-        m = __vmaxu2(__vmaxu2(m, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)),
-                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
-      }
-      m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
-      if (lane == 0) s_scale[t] = mi8_scale<true>(m << 16);
-    }
-    __syncthreads();
-  }
   if (!DOWN && blockIdx.x == 0)  // for kernel 2
     for (int i = threadIdx.x; i < (p.H + kI8Rows - 1) / kI8Rows; i += blockDim.x) p.count[i] = 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -326,10 +356,10 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   const int K = DOWN ? p.F : p.H;
   const int nk = (K + kI8KB - 1) / kI8KB;
   const int tiles = (p.F + 63) / 64;  // kernel 1
-  const int units = DOWN ? r.groups : r.groups * tiles;
   const int first = DOWN ? (int)(blockIdx.x % (unsigned)p.split) : (int)blockIdx.x;
+  const int col0 = DOWN ? (int)(blockIdx.x / (unsigned)p.split) * kI8Rows : 0;  // (past H: a spare CTA of the last cluster)
+  const int units = DOWN ? (col0 < p.H ? r.groups : 0) : r.groups * tiles;
   const int step = DOWN ? p.split : (int)gridDim.x;
-  const int col0 = DOWN ? (int)(blockIdx.x / (unsigned)p.split) * kI8Rows : 0;
   auto group_of = [&](int u) { return DOWN ? u : u / tiles; };
   // scale of row j of a group that starts at row0
   auto row_scale = [&](int row0, int j) { return s_scale[DOWN ? row0 + j : r.row_token[row0 + j]]; };
@@ -393,6 +423,8 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   } else if (warp < 6) {
     // ---------------- epilogue ----------------
     const int q = warp & 3;
+    if (DOWN)
+      for (int t = 0; t < p.M; ++t) ysum[t * kI8Rows + 32 * q + lane] = 0.f;  // this thread's column
     int done = 0;
     for (int u = first; u < units; u += step, ++done) {
       const int a = done & 1;
@@ -448,16 +480,22 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   } else {
     // ---------------- digits ----------------
     const int me = warp - 6;
+    // first the rows' scales (the weights' stream is under way)
     if (DOWN) {
       asm volatile("griddepcontrol.wait;" ::: "memory");  // h is kernel 1's
-      for (int row = threadIdx.x - 6 * 32; row < p.M * p.topk; row += 32 * kMi8DigitWarps) {
-        uint32_t m = 0;
-#pragma unroll 4
-        for (int i = 0; i < p.hparts; i += 4) {
-          const uint4 h = __ldcg(reinterpret_cast<const uint4*>(p.hmax + (int64_t)row * p.hparts + i));
-          m = max(max(m, max(h.x, h.y)), max(h.z, h.w));
+      // 16 of this CTA's groups at a time, 8 threads a group
+      for (int u = first + (threadIdx.x - 6 * 32) / 8 * step; u < units; u += 4 * kMi8DigitWarps * step) {
+        const int row0 = r.group_row[u] & 0xFFFF, rows = r.group_row[u] >> 16;
+        for (int j = threadIdx.x % 8; j < rows; j += 8) {
+          const uint4* part = reinterpret_cast<const uint4*>(p.hmax + (int64_t)(row0 + j) * p.hparts);
+          uint32_t m = 0;
+#pragma unroll 12
+          for (int i = 0; i < p.hparts / 4; ++i) {
+            const uint4 h = __ldcg(part + i);
+            m = max(max(m, max(h.x, h.y)), max(h.z, h.w));
+          }
+          s_scale[row0 + j] = mi8_scale<false>(m);
         }
-        s_scale[row] = mi8_scale<false>(m);
       }
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kMi8DigitWarps) : "memory");
     }
@@ -522,6 +560,7 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   if constexpr (DOWN) {
     // The last CTA of a column tile to arrive adds the splits' sums, in their order.
     __shared__ int s_last;
+    if (col0 >= p.H) return;
     const int tile = col0 / kI8Rows, n = p.M * kI8Rows;
     if (p.split > 1) {
       float* mine = p.part + ((int64_t)tile * p.split + first) * n;

@@ -522,8 +522,8 @@ q4k_status i8_gemm_t(const int8_t* W, const int8_t* X, I8GemmParams p, cudaStrea
                    smem_set[0], s);
 }
 
-// Shared memory of the layer's kernels: for few tokens half of an SM's, so that a CTA of
-// kernel 2 finds room beside one of kernel 1; else all of it.
+// Shared memory of the layer's kernels: half of an SM's, so that a CTA of kernel 2 finds
+// room beside one of kernel 1; all of it where half holds too few stages.
 template <int PL, bool DOWN>
 q4k_status launch_mi8_t(const CUtensorMap& tw, Mi8Params p, int grid, cudaStream_t s) {
   auto* k = mi8_kernel<PL, DOWN>;
@@ -534,11 +534,24 @@ q4k_status launch_mi8_t(const CUtensorMap& tw, Mi8Params p, int grid, cudaStream
   for (size_t budget : {kGemvTwoPerSm, (size_t)232448}) {
     smem = budget - fixed;
     p.stages = std::min<int>(kMi8MaxStages, (int)((smem - 1024 - ysum) / stage));
-    if (p.M <= 8 && p.stages >= kMi8DigitWarps) break;
+    if (p.stages >= kMi8DigitWarps) break;
   }
-  if (p.stages < kMi8DigitWarps) return Q4K_ERR_UNSUPPORTED;  // (does not happen: M <= 32)
   if (ensure_smem(k, 232448 - fixed, smem_set) != cudaSuccess) return launch_status(cudaErrorUnknown);
-  return launch_pdl_smem(k, dim3((unsigned)grid), dim3(32 * kMi8Warps), smem, s, tw, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(32 * kMi8Warps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kMi8Cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return launch_status(cudaLaunchKernelEx(&cfg, k, tw, p));
 }
 
 // CTAs per column tile of kernel 2: as many as keep one CTA per SM, at most one per expert.
@@ -552,10 +565,13 @@ q4k_status launch_mi8(Mi8Params p, const int8_t* Wgu, const int8_t* Wd, cudaStre
   CUtensorMap tgu, td;
   if (!make_tmap_gate_up(&tgu, Wgu, p.E, p.F, p.H) || !make_tmap_i8(&td, Wd, (int64_t)p.E * p.H, p.F, kI8Rows))
     return Q4K_ERR_CUDA;
-  const int64_t most = (int64_t)std::min(p.E, p.M * p.topk) * mi8_tiles(p.F);  // units of kernel 1 at most
-  const q4k_status st = launch_mi8_t<PL, false>(tgu, p, (int)std::min<int64_t>(most, sm_count()), s);
+  // whole clusters; one CTA per SM, no more than units
+  const int64_t most = (int64_t)p.M * p.topk * mi8_tiles(p.F);
+  auto whole = [](int64_t n) { return (int)((n + kMi8Cluster - 1) / kMi8Cluster * kMi8Cluster); };
+  const q4k_status st =
+      launch_mi8_t<PL, false>(tgu, p, whole(std::min<int64_t>(most, sm_count() / kMi8Cluster * kMi8Cluster)), s);
   if (st != Q4K_OK) return st;
-  return launch_mi8_t<PL, true>(td, p, (p.H + kI8Rows - 1) / kI8Rows * p.split, s);
+  return launch_mi8_t<PL, true>(td, p, whole((int64_t)((p.H + kI8Rows - 1) / kI8Rows) * p.split), s);
 }
 
 }  // namespace
@@ -857,8 +873,9 @@ q4k_status moe_i8_layer(const float* logits, int M, int E, int topk, const int8_
   p.residual = residual;
   p.Y = Y;
   p.hparts = 4 * mi8_tiles(F);
-  p.h = static_cast<float*>(ws);
-  uint8_t* w = static_cast<uint8_t*>(ws) + mi8_ws_h(M, topk, F);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.h = reinterpret_cast<float*>(w);
+  w += mi8_ws_h(M, topk, F);
   p.hmax = reinterpret_cast<uint32_t*>(w);
   p.count = reinterpret_cast<int32_t*>(w += mi8_ws_hmax(M, topk, F));
   p.part = reinterpret_cast<float*>(w + ((H + kI8Rows - 1) / kI8Rows + 3) / 4 * 16);
@@ -868,7 +885,7 @@ q4k_status moe_i8_layer(const float* logits, int M, int E, int topk, const int8_
   p.topk = topk;
   p.H = H;
   p.F = F;
-  p.nb = (4 * M + 15) / 16 * 16;
+  p.nb = (4 * std::min(M, kMi8GroupRows) + 15) / 16 * 16;
   p.tstride = (p.nb + 31) / 32 * 32;
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.tstride) p.tmem_cols *= 2;
