@@ -13,12 +13,19 @@
 // channel, so a warp stores 32 neighbouring channels of a token at once, whatever N is.
 //   warp 0     TMA producer: 128 bytes of K of the weight and token tiles per stage
 //              (128-byte swizzle; rows and columns past the ends arrive as zeros).
-//   warp 1     allocates TMEM; one lane issues tcgen05.mma kind::i8 (M=128, N=NT, K=32).
-//   warps 2-5  epilogue: tcgen05.ld, scales, store.
+//   warp 1     allocates TMEM; one lane issues tcgen05.mma kind::i8 (N=NT, K=32).
+//   warps 2-9  epilogue: tcgen05.ld, scales, store; two warps per TMEM quadrant, taking the
+//              token columns 16 at a time in turn.
 // A CTA walks tiles with two accumulators, so that a tile's epilogue runs under the next
-// one's MMAs. With too few tiles for the GPU a cluster of up to eight CTAs splits K
-// (SPLIT): every CTA sends each peer that peer's share of the token columns through
-// distributed shared memory, and sums and stores its own share.
+// one's MMAs.
+// PAIR: a CTA pair computes 256 weight rows x NT tokens with cta_group::2 (each CTA its 128
+// rows and half of the token tile, which both read): a lone CTA has to pull (128 + NT) x 128
+// bytes per stage from L2, more than the ~64 bytes a cycle that an SM gets while its MMAs
+// take 2 NT cycles; a pair (128 + NT / 2) x 128. The odd CTA's copies signal the even CTA's
+// barriers, whose MMA lane issues for both.
+// SPLIT: with too few tiles for the GPU the CTAs (or pairs) of a cluster split K: every CTA
+// sends each other one of its share of the token columns through distributed shared
+// memory, and sums and stores its own share.
 // SwiGLU tiles hold 64 gate and the matching 64 up rows, 16 of each per warp's 32 lanes, so
 // that one shuffle brings a gate and its up value together.
 // Every wait is bounded; on expiry the kernel latches Q4K_ERR_DEVICE_TIMEOUT, stops all
@@ -33,7 +40,8 @@ constexpr int kI8Rows = 128;       // weight rows of a tile
 constexpr int kI8KB = 128;         // bytes of K per stage
 constexpr int kI8MaxNT = 256;      // tokens of a tile
 constexpr int kI8MaxStages = 12;
-constexpr int kI8Threads = 192;
+constexpr int kI8EpiWarps = 8;
+constexpr int kI8Threads = 32 * (2 + kI8EpiWarps);
 constexpr uint32_t kI8ATile = kI8Rows * kI8KB;
 // |acc| <= 128 * 128 * K < 2^31
 constexpr int kI8MaxK = 131056;
@@ -47,7 +55,7 @@ struct I8GemmParams {
   int n_tiles;   // tiles along the weight rows
   int m_tiles;
   int stages;
-  int csplit;    // CTAs of a cluster that split K (SPLIT)
+  int ksplit;    // CTAs (pairs) of a cluster that split K (SPLIT)
   int tstride;   // TMEM columns between the two accumulators (a multiple of 32)
   int tmem_cols; // columns to allocate: two accumulators (SPLIT: one), a power of two
   int tail;      // shared-memory offset of barriers and scales
@@ -74,8 +82,52 @@ __device__ __forceinline__ void umma_i8(uint32_t tmem_d, uint64_t adesc, uint64_
       : "memory");
 }
 
+// The pair's MMA (see umma2_f16kind).
+__device__ __forceinline__ void umma2_i8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Completion of the MMAs issued so far, signalled on the barrier at this offset in the
+// CTAs of the cluster that `mask` names.
+__device__ __forceinline__ void umma2_commit(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+
+// As tma_load_2d / tma_load_gate_up, for a CTA of a pair: `bar` (a cluster address) may be the
+// peer's.
+__device__ __forceinline__ void tma2_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma2_load_gate_up(uint32_t dst, const CUtensorMap* map, int x, int r16, int e,
+                                                  uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+      "[%1, {%2, %3, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(r16), "r"(e), "r"(bar)
+      : "memory");
+}
+
+// silu(g) * u as silu_mul, the quotient by a reciprocal: 1 + e lies in [1, 2], where
+// __fdividef is within 2 ulp.
+__device__ __forceinline__ float i8_silu_mul(float g, float u) {
+  const float e = expf(-fabsf(g));
+  return g * __fdividef(g >= 0.f ? 1.f : e, 1.f + e) * u;
+}
+
 // Instruction descriptor of kind::i8: int32 accumulators (2), signed A and B (1), both
-// K-major, M = 128, N = nt.
+// K-major.
 __host__ __device__ __forceinline__ uint32_t i8_idesc(int m, int nt) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(nt >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
@@ -89,12 +141,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, int32_t (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void st_cluster_s32(uint32_t saddr, uint32_t rank, int32_t v) {
-  asm volatile(
-      "{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, %1;\n"
-      " st.shared::cluster.b32 [ra], %2;\n}" ::"r"(saddr),
-      "r"(rank), "r"(v)
-      : "memory");
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, int32_t a, int32_t b, int32_t c, int32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // A place in a ring of stages, and the parity of its pass (the roles' single threads pay
@@ -130,15 +183,21 @@ __device__ __forceinline__ int i8_row(int n_tile, int q, int lane, bool* up) {
   return n_tile * (kI8Rows / 2) + 16 * q + (lane & 15);
 }
 
-template <bool SWIGLU, bool BF16, bool SPLIT>
+// Words between the rows of a SPLIT share of `per` (a multiple of 4) token columns: an odd
+// number of 16-byte pieces, so that eight rows' pieces lie in different banks.
+__host__ __device__ __forceinline__ int i8_part_pitch(int per) { return per / 4 % 2 ? per : per + 4; }
+
+template <bool SWIGLU, bool BF16, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(kI8Threads)
 i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x, I8GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t stage_bytes = kI8ATile + (uint32_t)p.nt * kI8KB;
+  constexpr int P = PAIR ? 2 : 1;
+  const uint32_t stage_bytes = kI8ATile + (uint32_t)(p.nt / P) * kI8KB;
 
+  // barriers; full and tempty of a pair are the even CTA's
   const uint32_t bars = sbase + (uint32_t)p.tail;
   auto bar_full = [&](int s) { return bars + 8u * s; };
   auto bar_empty = [&](int s) { return bars + 8u * (kI8MaxStages + s); };
@@ -146,7 +205,13 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
   auto bar_tempty = [&](int a) { return bars + 8u * (2 * kI8MaxStages + 2 + a); };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + p.tail + 8 * (2 * kI8MaxStages + 4));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + p.tail + 8 * (2 * kI8MaxStages + 4) + 4);
-  float* s_xs = reinterpret_cast<float*>(smem + p.tail + 256);  // [4 warps][kI8MaxNT] token scales
+  float* s_xs = reinterpret_cast<float*>(smem + p.tail + 256);  // [epilogue warps][kI8MaxNT] token scales
+
+  // place in the cluster: ranks P s + r: half r of the pair, share s of K
+  const int csize = SPLIT ? P * p.ksplit : P;
+  const int rank = (int)(blockIdx.x % (unsigned)csize);
+  const int r = rank % P, ks = rank / P;
+  const uint32_t leader = (uint32_t)(rank - r);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -155,35 +220,45 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar_tfull(a), 1);
-      mbar_init(bar_tempty(a), 4);
+      mbar_init(bar_tempty(a), P * kI8EpiWarps);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(const_cast<uint32_t*>(tmem_slot))), "r"((uint32_t)p.tmem_cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    const uint32_t slot = smem_u32(const_cast<uint32_t*>(tmem_slot)), cols = (uint32_t)p.tmem_cols;
+    if (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if (PAIR)
+    cluster_barrier();  // the peer's barriers and TMEM are ready too
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // everything above ran under the previous kernel; its results are read from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // SPLIT: one tile per cluster, this CTA's share of K; else this CTA's tiles, all of K
+  // SPLIT: one tile per cluster, this CTA's share of K; else the CTA's (pair's) tiles, all of K
   const int tiles = p.n_tiles * p.m_tiles;
-  const int rank = SPLIT ? (int)(blockIdx.x % (unsigned)p.csplit) : 0;
-  const int first = SPLIT ? (int)(blockIdx.x / (unsigned)p.csplit) : (int)blockIdx.x;
-  const int step = SPLIT ? tiles : (int)gridDim.x;
+  const int first = (int)(blockIdx.x / (unsigned)csize);
+  const int step = SPLIT ? tiles : (int)(gridDim.x / (unsigned)P);
   const int nk_all = (p.K + kI8KB - 1) / kI8KB;
-  const int k0 = SPLIT ? (int)((int64_t)nk_all * rank / p.csplit) : 0;
-  const int nk = SPLIT ? (int)((int64_t)nk_all * (rank + 1) / p.csplit) - k0 : nk_all;  // >= 1
+  const int k0 = SPLIT ? (int)((int64_t)nk_all * ks / p.ksplit) : 0;
+  const int nk = SPLIT ? (int)((int64_t)nk_all * (ks + 1) / p.ksplit) - k0 : nk_all;  // >= 1
   const int half = p.N / 2;
   const uint64_t limit = *const_cast<volatile unsigned long long*>(&g_wait_limit_ns);
+  // a tile's first token and this CTA's tile of weight rows
+  auto tile_m0 = [&](int tile) { return tile % p.m_tiles * p.nt; };
+  auto tile_n = [&](int tile) { return tile / p.m_tiles * P + r; };
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -193,46 +268,63 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
       I8Ring at;
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += step) {
-        const int m0 = tile % p.m_tiles * p.nt, nti = tile / p.m_tiles;
+        const int m0 = tile_m0(tile) + r * (p.nt / P), nti = tile_n(tile);
         for (int k = 0; k < nk; ++k, ++it, at.next(p.stages)) {
           const int s = at.s;
           // (a barrier's phase before its first counts as complete)
           if (!(ok = mbar_wait_l(bar_empty(s), at.parity ^ 1, abort_flag, limit))) break;
           if (it == drop) continue;  // test hook: this stage never arrives
-          mbar_arrive_expect_tx(bar_full(s), stage_bytes);
+          if (r == 0) mbar_arrive_expect_tx(bar_full(s), P * stage_bytes);
           const uint32_t a_dst = sbase + s * stage_bytes;
+          const uint32_t bar = PAIR ? cluster_addr(bar_full(s), leader) : bar_full(s);
           const int x = (k0 + k) * kI8KB;
+          auto load = [&](uint32_t dst, const CUtensorMap* map, int y) {
+            if (PAIR)
+              tma2_load_2d(dst, map, x, y, bar);
+            else
+              tma_load_2d(dst, map, x, y, bar);
+          };
           if (SWIGLU && p.boxed) {
-            tma_load_gate_up(a_dst, &tmap_w, x, nti * 4, 0, bar_full(s));
+            if (PAIR)
+              tma2_load_gate_up(a_dst, &tmap_w, x, nti * 4, 0, bar);
+            else
+              tma_load_gate_up(a_dst, &tmap_w, x, nti * 4, 0, bar);
           } else if (SWIGLU) {
             const int f0 = nti * (kI8Rows / 2);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              tma_load_2d(a_dst + (uint32_t)(32 * q) * kI8KB, &tmap_w, x, f0 + 16 * q, bar_full(s));
-              tma_load_2d(a_dst + (uint32_t)(32 * q + 16) * kI8KB, &tmap_w, x, half + f0 + 16 * q, bar_full(s));
+              load(a_dst + (uint32_t)(32 * q) * kI8KB, &tmap_w, f0 + 16 * q);
+              load(a_dst + (uint32_t)(32 * q + 16) * kI8KB, &tmap_w, half + f0 + 16 * q);
             }
           } else {
-            tma_load_2d(a_dst, &tmap_w, x, nti * kI8Rows, bar_full(s));
+            load(a_dst, &tmap_w, nti * kI8Rows);
           }
-          tma_load_2d(a_dst + kI8ATile, &tmap_x, x, m0, bar_full(s));
+          load(a_dst + kI8ATile, &tmap_x, m0);
         }
       }
       // every issued stage lands before this CTA may exit (on the normal path the MMA
-      // role has waited for all of them)
-      if (*abort_flag)
-        for (int i = max(0, it - p.stages); i < it; ++i)
-          if (i != drop) mbar_wait_drain(bar_full(i % p.stages), (i / p.stages) & 1);
+      // role has waited for all of them; of a pair, the even CTA's barriers tell)
+      if (*abort_flag && r == 0) {
+        I8Ring back;
+        for (int i = 0; i < it; ++i, back.next(p.stages))
+          if (i >= it - p.stages && i != drop) mbar_wait_drain(bar_full(back.s), back.parity);
+      }
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      const uint32_t idesc = i8_idesc(kI8Rows, p.nt);
+    // ---------------- MMA issuer (of a pair: the even CTA's) ----------------
+    if (lane == 0 && r == 0) {
+      const uint32_t idesc = i8_idesc(P * kI8Rows, p.nt);
+      const uint16_t both = (uint16_t)(3u << leader);
       int done = 0;
       I8Ring at;
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += step, ++done) {
         const int a = done & 1;
-        if (done >= 2 && !(ok = mbar_wait_l(bar_tempty(a), (done / 2 - 1) & 1, abort_flag, limit))) break;
+        if (done >= 2) {
+          ok = PAIR ? mbar_wait_cluster(bar_tempty(a), (done / 2 - 1) & 1, abort_flag)
+                    : mbar_wait_l(bar_tempty(a), (done / 2 - 1) & 1, abort_flag, limit);
+          if (!ok) break;
+        }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(a * p.tstride);
         for (int k = 0; k < nk; ++k, at.next(p.stages)) {
@@ -241,33 +333,41 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
           const uint32_t a0 = sbase + at.s * stage_bytes;
           const uint64_t ad = umma_desc_sw128(a0), bd = umma_desc_sw128(a0 + kI8ATile);
 #pragma unroll
-          for (int kk = 0; kk < kI8KB / 32; ++kk)  // 32 bytes of K on: 2 in the descriptors' units
-            umma_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
-          umma_commit(bar_empty(at.s));
+          for (int kk = 0; kk < kI8KB / 32; ++kk) {  // 32 bytes of K on: 2 in the descriptors' units
+            if (PAIR)
+              umma2_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
+            else
+              umma_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
+          }
+          if (PAIR)
+            umma2_commit(bar_empty(at.s), both);
+          else
+            umma_commit(bar_empty(at.s));
         }
-        if (ok) umma_commit(bar_tfull(a));
+        if (ok && PAIR) umma2_commit(bar_tfull(a), both);
+        if (ok && !PAIR) umma_commit(bar_tfull(a));
       }
     }
   } else if (!SPLIT) {
     // ---------------- epilogue ----------------
-    const int q = warp & 3;
+    const int q = warp & 3, turn = (warp - 2) >> 2;
     int done = 0;
     const int64_t ldy = SWIGLU ? half : p.N;
     const int rows = SWIGLU ? half : p.N;
+    float* xs = s_xs + (warp - 2) * kI8MaxNT;  // a copy per warp: no barrier between warps, which may stop apart
     for (int tile = first; tile < tiles; tile += step, ++done) {
       const int a = done & 1;
-      const int m0 = tile % p.m_tiles * p.nt, nti = tile / p.m_tiles;
+      const int m0 = tile_m0(tile);
       const int mcount = min(p.nt, p.M - m0);
-      float* xs = s_xs + q * kI8MaxNT;  // a copy per warp: no barrier between warps, which may stop apart
       for (int i = lane; i < p.nt; i += 32) xs[i] = i < mcount ? p.xs[m0 + i] : 0.f;
       bool up;
-      const int r = i8_row<SWIGLU>(nti, q, lane, &up);
-      const float w = r < rows ? p.ws[up ? half + r : r] : 0.f;
+      const int n = i8_row<SWIGLU>(tile_n(tile), q, lane, &up);
+      const float w = n < rows ? p.ws[up ? half + n : n] : 0.f;
       __syncwarp();
       if (!__all_sync(0xffffffffu, mbar_wait_l(bar_tfull(a), (done / 2) & 1, abort_flag, limit))) break;
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * p.tstride);
-      for (int c = 0; c < mcount; c += 16) {
+      for (int c = 16 * turn; c < mcount; c += 16 * (kI8EpiWarps / 4)) {
         int32_t v[16];
         tmem_ld16(d + c, v);
         if (SWIGLU) {
@@ -275,48 +375,64 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
           for (int i = 0; i < 16; i += 2) {
             const float y0 = (float)v[i] * xs[c + i] * w, y1 = (float)v[i + 1] * xs[c + i + 1] * w;
             const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
-            const float hv = up ? silu_mul(got, y1) : silu_mul(y0, got);
+            const float hv = up ? i8_silu_mul(got, y1) : i8_silu_mul(y0, got);
             const int m = c + i + (up ? 1 : 0);
-            if (m < mcount && r < rows) i8_store<BF16>(p.Y, (int64_t)(m0 + m) * ldy + r, hv);
+            if (m < mcount && n < rows) i8_store<BF16>(p.Y, (int64_t)(m0 + m) * ldy + n, hv);
           }
-        } else if (r < rows) {
+        } else if (n < rows) {
+          const int64_t at = (int64_t)(m0 + c) * ldy + n;
+          if (c + 16 <= mcount) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < mcount) i8_store<BF16>(p.Y, (int64_t)(m0 + c + i) * ldy + r, (float)v[i] * xs[c + i] * w);
+            for (int i = 0; i < 16; ++i) i8_store<BF16>(p.Y, at + i * ldy, (float)v[i] * xs[c + i] * w);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c + i < mcount) i8_store<BF16>(p.Y, at + i * ldy, (float)v[i] * xs[c + i] * w);
+          }
         }
         __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_tempty(a));
+      if (lane == 0) {
+        if (PAIR)
+          mbar_arrive_remote(bar_tempty(a), leader);
+        else
+          mbar_arrive(bar_tempty(a));
+      }
     }
   }
 
   if constexpr (SPLIT) {
-    // ---------------- reduction over the cluster ----------------
-    const int tile = first;
-    const int m0 = tile % p.m_tiles * p.nt, nti = tile / p.m_tiles;
+    // ---------------- reduction over the CTAs that share the tile's rows ----------------
+    const int m0 = tile_m0(first), nti = tile_n(first);
     const int mcount = min(p.nt, p.M - m0);
-    const int per = (p.nt + p.csplit - 1) / p.csplit;  // token columns that a CTA sums and stores
-    int32_t* part = reinterpret_cast<int32_t*>(smem);  // [csplit][per][128]: the stages are free by then
-    const int q = warp & 3;
+    const int per = ((p.nt + p.ksplit - 1) / p.ksplit + 3) / 4 * 4;  // token columns that a CTA sums and stores
+    const int pitch = i8_part_pitch(per);
+    int32_t* part = reinterpret_cast<int32_t*>(smem);  // [ksplit][128][pitch]: the stages are free by then
+    const int q = warp & 3, turn = (warp - 2) >> 2;
     bool ok = true;
-    if (warp >= 2) ok = __all_sync(0xffffffffu, mbar_wait_l(bar_tfull(0), 0, abort_flag, limit));
+    if (warp >= 2) {
+      for (int i = threadIdx.x - 64; i < mcount; i += 32 * kI8EpiWarps) s_xs[i] = p.xs[m0 + i];
+      ok = __all_sync(0xffffffffu, mbar_wait_l(bar_tfull(0), 0, abort_flag, limit));
+    }
     __syncwarp();
     cluster_barrier();  // no CTA's MMAs read its stages any more
     if (warp >= 2 && ok) {
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16);
-      for (int c = 0; c < mcount; c += 16) {
+      const uint32_t mine = sbase + (uint32_t)((ks * kI8Rows + 32 * q + lane) * pitch) * 4u;
+      int to = 16 * turn / per, left = 16 * turn % per;  // whose column comes next, and where in the share
+      for (int c = 16 * turn; c < mcount; c += 16 * (kI8EpiWarps / 4)) {
         int32_t v[16];
         tmem_ld16(d + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int col = c + i;
-          if (col < mcount)
-            st_cluster_s32(smem_u32(part + ((int64_t)rank * per + col % per) * kI8Rows + 32 * q + lane),
-                           (uint32_t)(col / per), v[i]);
+        for (int i = 0; i < 16; i += 4) {
+          if (c + i < mcount)
+            st_cluster_v4(cluster_addr(mine + 4u * left, (uint32_t)(P * to + r)), v[i], v[i + 1], v[i + 2], v[i + 3]);
+          if ((left += 4) >= per) left -= per, ++to;
         }
+        for (left += 16 * (kI8EpiWarps / 4 - 1); left >= per; left -= per) ++to;
       }
       tc_fence_before();
     }
@@ -324,31 +440,30 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
     cluster_barrier();
     if (warp >= 2 && ok) {
       const int et = threadIdx.x - 64;
-      const int c1 = min(per, mcount - rank * per);
-      auto sum = [&](int c, int row) {
-        int32_t t = 0;
-        for (int s = 0; s < p.csplit; ++s) t += part[(s * per + c) * kI8Rows + row];
-        return (float)t;
-      };
-      if (SWIGLU) {
-        const int f = nti * (kI8Rows / 2) + (et & 63);
-        const int row = 32 * ((et & 63) >> 4) + (et & 15);
-        if (f < half) {
-          const float wg = p.ws[f], wu = p.ws[half + f];
-          for (int c = et >> 6; c < c1; c += 2) {
-            const int m = m0 + rank * per + c;
-            const float xs = p.xs[m];
-            i8_store<BF16>(p.Y, (int64_t)m * half + f, silu_mul(sum(c, row) * xs * wg, sum(c, row + 16) * xs * wu));
-          }
+      const int c0 = ks * per, c1 = min(per, mcount - c0);  // this CTA's columns of the tile
+      auto sum = [&](int c, int row, float (&y)[4]) {
+        int32_t t[4] = {0, 0, 0, 0};
+        for (int s = 0; s < p.ksplit; ++s) {
+          const int4 v = *reinterpret_cast<const int4*>(part + (s * kI8Rows + row) * pitch + c);
+          t[0] += v.x, t[1] += v.y, t[2] += v.z, t[3] += v.w;
         }
-      } else {
-        const int n = nti * kI8Rows + et;
-        if (n < p.N) {
-          const float w = p.ws[n];
-          for (int c = 0; c < c1; ++c) {
-            const int m = m0 + rank * per + c;
-            i8_store<BF16>(p.Y, (int64_t)m * p.N + n, sum(c, et) * p.xs[m] * w);
-          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = (float)t[i] * s_xs[min(c0 + c + i, mcount - 1)];
+      };
+      constexpr int kCols = SWIGLU ? 64 : 128, kStep = 32 * kI8EpiWarps / kCols * 4;
+      const int n = nti * kCols + et % kCols;
+      const int64_t ldy = SWIGLU ? half : p.N;
+      if (n < (SWIGLU ? half : p.N)) {
+        const float w = p.ws[n], wu = SWIGLU ? p.ws[half + n] : 0.f;
+        const int row = SWIGLU ? 32 * (et % 64 / 16) + et % 16 : et % 128;
+        for (int c = et / kCols * 4; c < c1; c += kStep) {
+          float y[4], u[4];
+          sum(c, row, y);
+          if (SWIGLU) sum(c, row + 16, u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < c1)
+              i8_store<BF16>(p.Y, (int64_t)(m0 + c0 + c + i) * ldy + n, SWIGLU ? i8_silu_mul(y[i] * w, u[i] * wu) : y[i] * w);
         }
       }
     }
@@ -356,12 +471,18 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
 
   // ---- teardown ----
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if (PAIR)
+    cluster_barrier();  // neither CTA leaves while the pair's MMAs, copies or arrivals may touch it
+  else
+    __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)p.tmem_cols)
-                 : "memory");
+    if (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)p.tmem_cols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)p.tmem_cols) : "memory");
   }
 }
 

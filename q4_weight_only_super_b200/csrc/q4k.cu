@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "common.cuh"
@@ -430,13 +431,10 @@ q4k_status noalloc_route_scratch(int32_t** out) {
 
 // ------------------------------------------------------------ int8 products ----
 
-// Shared memory of one product CTA: the whole SM's for tiles of many tokens, half of it
-// (two CTAs per SM) for narrow ones, whose accumulators then fit half the TMEM too.
+// Shared memory of one product CTA: the whole SM's, or half of it (two CTAs per SM) for
+// lone CTAs on narrow token tiles, whose accumulators then fit half the TMEM too.
 constexpr size_t kI8Smem[2] = {232448, kGemvTwoPerSm};
-constexpr size_t kI8TailBytes = 256 + 4 * kI8MaxNT * sizeof(float);
-
-// g_i8_fit[d][h][c]: clusters of c product CTAs (h: two CTAs per SM) resident at once.
-std::atomic<int> g_i8_fit[kMaxDevices][2][9];
+constexpr size_t kI8TailBytes = 256 + kI8EpiWarps * kI8MaxNT * sizeof(float);
 
 template <typename F>
 q4k_status i8_launch(F* k, const CUtensorMap& tw, const CUtensorMap& tx, const I8GemmParams& p, int grid, int cluster,
@@ -448,16 +446,14 @@ q4k_status i8_launch(F* k, const CUtensorMap& tw, const CUtensorMap& tx, const I
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   if (fit) {
-    cfg.attrs = attr + 1;
+    cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(fit, k, &cfg) != cudaSuccess || *fit <= 0) {
       cudaGetLastError();
@@ -465,61 +461,115 @@ q4k_status i8_launch(F* k, const CUtensorMap& tw, const CUtensorMap& tx, const I
     }
     return Q4K_OK;
   }
+  cfg.attrs = cluster > 1 ? attr : attr + 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return launch_status(cudaLaunchKernelEx(&cfg, k, tw, tx, p));
 }
 
+// g_i8_fit[d][c]: clusters of c product CTAs resident at once, one CTA per SM.
+std::atomic<int> g_i8_fit[kMaxDevices][9];
 std::atomic<size_t> g_i8_smem_fit[kMaxDevices];
 
-int i8_cluster_fit(int halved, int c) {
+int i8_cluster_fit(int c) {
   const int dev = current_device();
   if (dev < 0 || dev >= kMaxDevices) return 0;
-  int v = g_i8_fit[dev][halved][c].load();
+  int v = g_i8_fit[dev][c].load();
   if (v <= 0) {
     CUtensorMap none = {};
-    i8_launch(i8_gemm_kernel<false, false, true>, none, none, I8GemmParams{}, 64 * c, c, kI8Smem[halved],
+    i8_launch(i8_gemm_kernel<false, false, false, true>, none, none, I8GemmParams{}, 64 * c, c, kI8Smem[0],
               g_i8_smem_fit, nullptr, &v);
-    g_i8_fit[dev][halved][c].store(v);
+    g_i8_fit[dev][c].store(v);
   }
   return v;
+}
+
+// How a product is cut: pairs or lone CTAs, token tiles, shares of K.
+struct I8Cut {
+  int pair, halved, m_tiles, nt, n_tiles, ksplit, stages;
+};
+
+// The cut with the least estimated time, in SM cycles. A stage (128 bytes of K of a CTA's
+// tiles) takes 2 cycles a token for the MMAs, or its bytes at ~56 a cycle from L2, and not
+// less than the ring's latency allows; the weights and tokens come from DRAM at ~3100 bytes a
+// cycle; a K split pays for its exchange.
+I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
+  const int nk = (K + kI8KB - 1) / kI8KB;
+  const double dram = ((double)rows * (kI8Rows / tile_rows) + M) * K / 3100.;
+  I8Cut best = {};
+  double least = 1e300;
+  for (int pair = 0; pair < 2; ++pair) {
+    const int P = pair + 1, grain = 16 * P;
+    const int fewest = (M + kI8MaxNT - 1) / kI8MaxNT;
+    for (int mt = fewest; mt < fewest + 3; ++mt) {
+      I8Cut c = {};
+      c.pair = pair;
+      c.m_tiles = mt;
+      c.nt = ((M + mt - 1) / mt + grain - 1) / grain * grain;
+      c.n_tiles = (rows + tile_rows * P - 1) / (tile_rows * P);
+      c.halved = !pair && c.nt <= 128;
+      const size_t stage = kI8ATile + (size_t)(c.nt / P) * kI8KB;
+      c.stages = std::min<int>(kI8MaxStages, (int)((kI8Smem[c.halved] - 1024 - kI8TailBytes) / stage));
+      const double tiles = (double)c.n_tiles * mt;
+      const double work = std::max(2. * c.nt, stage / 56.), ring = 1400. / std::min(c.stages, 4);
+      for (int ks = 1; ks <= std::min(8 / P, nk); ++ks) {
+        c.ksplit = ks;
+        const double ctas = tiles * P * ks;
+        if (ks > 1) {
+          const int per = ((c.nt + ks - 1) / ks + 3) / 4 * 4;
+          if (tiles > (double)i8_cluster_fit(P * ks) * (1 + c.halved)) continue;
+          if ((size_t)ks * kI8Rows * i8_part_pitch(per) * 4 > c.stages * stage) continue;
+        }
+        const double waves = std::ceil(ctas / (sms * (1 + c.halved)));
+        const double share = c.halved && ctas > sms ? 2 : 1;
+        const double mma = waves * std::ceil((double)nk / ks) * std::max(share * work, ring);
+        const double t = std::max(mma, dram) + 0.15 * std::min(mma, dram) + (ks > 1 ? 3000. + 10. * c.nt : 6. * c.nt);
+        if (t < least) {
+          least = t;
+          best = c;
+        }
+      }
+    }
+  }
+  return best;
+}
+
+template <bool SWIGLU, bool BF16, bool PAIR>
+q4k_status i8_gemm_cut(const I8Cut& c, const CUtensorMap& tw, const CUtensorMap& tx, const I8GemmParams& p, int sms,
+                       cudaStream_t s) {
+  constexpr int P = PAIR ? 2 : 1;
+  static std::atomic<size_t> smem_set[2][kMaxDevices];
+  const int tiles = c.n_tiles * c.m_tiles;
+  const size_t smem = kI8Smem[c.halved];
+  if (c.ksplit > 1)
+    return i8_launch(i8_gemm_kernel<SWIGLU, BF16, PAIR, true>, tw, tx, p, tiles * P * c.ksplit, P * c.ksplit, smem,
+                     smem_set[1], s);
+  return i8_launch(i8_gemm_kernel<SWIGLU, BF16, PAIR, false>, tw, tx, p,
+                   std::min(tiles, sms * (1 + c.halved) / P) * P, P, smem, smem_set[0], s);
 }
 
 template <bool SWIGLU, bool BF16>
 q4k_status i8_gemm_t(const int8_t* W, const int8_t* X, I8GemmParams p, cudaStream_t s) {
   const int sms = sm_count();
   if (sms <= 0) return Q4K_ERR_CUDA;
-  // token tiles of equal width, at most 256
-  p.m_tiles = (p.M + kI8MaxNT - 1) / kI8MaxNT;
-  p.nt = ((p.M + p.m_tiles - 1) / p.m_tiles + 15) / 16 * 16;
   const int rows = SWIGLU ? p.N / 2 : p.N, tile_rows = SWIGLU ? kI8Rows / 2 : kI8Rows;
-  p.n_tiles = (rows + tile_rows - 1) / tile_rows;
-  if ((int64_t)p.n_tiles * p.m_tiles > 0x7fffffffLL / 8) return Q4K_ERR_UNSUPPORTED;
-  const int tiles = p.n_tiles * p.m_tiles;
-  const int nk = (p.K + kI8KB - 1) / kI8KB;
+  if (((int64_t)rows / tile_rows + 2) * (p.M / 16 + 4) > 0x7fffffffLL / 16) return Q4K_ERR_UNSUPPORTED;
+  const I8Cut c = i8_cut(p.M, rows, tile_rows, p.K, sms);
+  p.nt = c.nt;
+  p.n_tiles = c.n_tiles;
+  p.m_tiles = c.m_tiles;
+  p.stages = c.stages;
+  p.ksplit = c.ksplit;
+  p.tail = c.stages * (int)(kI8ATile + (size_t)(c.nt / (1 + c.pair)) * kI8KB);
   p.tstride = (p.nt + 31) / 32 * 32;
-  const size_t stage = kI8ATile + (size_t)p.nt * kI8KB;
-  const int halved = p.nt <= 128;
-  const size_t smem = kI8Smem[halved];
-  p.stages = std::min<int>(kI8MaxStages, (int)((smem - 1024 - kI8TailBytes) / stage));
-  p.tail = (int)(p.stages * stage);
-  // K split over the largest cluster with which all tiles are resident at once
-  int c = 1;
-  for (int t = std::min(8, nk); t > 1; --t)
-    if (i8_cluster_fit(halved, t) >= tiles) {
-      c = t;
-      break;
-    }
-  p.csplit = c;
   p.tmem_cols = 32;
-  while (p.tmem_cols < (c > 1 ? 1 : 2) * p.tstride) p.tmem_cols *= 2;
+  while (p.tmem_cols < (c.ksplit > 1 ? 1 : 2) * p.tstride) p.tmem_cols *= 2;
   CUtensorMap tw, tx;
   p.boxed = SWIGLU && rows % 16 == 0;
-  if (!(p.boxed ? make_tmap_gate_up(&tw, W, 1, rows, p.K) : make_tmap_i8(&tw, W, p.N, p.K, SWIGLU ? 16 : kI8Rows)) || !make_tmap_i8(&tx, X, p.M, p.K, p.nt))
+  if (!(p.boxed ? make_tmap_gate_up(&tw, W, 1, rows, p.K) : make_tmap_i8(&tw, W, p.N, p.K, SWIGLU ? 16 : kI8Rows)) ||
+      !make_tmap_i8(&tx, X, p.M, p.K, p.nt / (1 + c.pair)))
     return Q4K_ERR_CUDA;
-  static std::atomic<size_t> smem_set[2][kMaxDevices];
-  if (c > 1)
-    return i8_launch(i8_gemm_kernel<SWIGLU, BF16, true>, tw, tx, p, tiles * c, c, smem, smem_set[1], s);
-  return i8_launch(i8_gemm_kernel<SWIGLU, BF16, false>, tw, tx, p, std::min(tiles, sms * (halved + 1)), 1, smem,
-                   smem_set[0], s);
+  return c.pair ? i8_gemm_cut<SWIGLU, BF16, true>(c, tw, tx, p, sms, s)
+                : i8_gemm_cut<SWIGLU, BF16, false>(c, tw, tx, p, sms, s);
 }
 
 // Shared memory of the layer's kernels: half of an SM's, so that a CTA of kernel 2 finds
