@@ -357,69 +357,59 @@ def moe_combine_residual(O, inv_perm, topk_w, residual, M: int, topk: int, H: in
     return Y
 
 
-def _need(fn, name, t, dtypes, shape, device):
-    """An operand of the int8 lane: a contiguous CUDA tensor of the right type, shape and device."""
-    if t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{fn}: {name} must be a contiguous {' or '.join(str(d) for d in dtypes)} tensor of shape "
-                         f"{shape} on {device}; got {t.dtype} {tuple(t.shape)} on {t.device}"
-                         f"{'' if t.is_contiguous() else ', not contiguous'}")
-
-
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _I8, _F32 = (torch.int8,), (torch.float32,)
 
 
-class _On:
-    """The device and stream a call of the int8 lane runs on: the operands' device made
-    current, and what the call allocates taken from its own stream's pool."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.ctx = device, stream, None
-
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(self.device)
-            self.ctx.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-
-    def empty(self, shape, dtype):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        s = self.stream
-        if isinstance(s, int):
-            s = torch.cuda.ExternalStream(s, device=self.device) if s else torch.cuda.default_stream(self.device)
-        with torch.cuda.stream(s):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+def _need(fn, name, t, dtypes, shape, dev):
+    """An operand of the int8 lane: contiguous, of the right type and shape, on CUDA device `dev`."""
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev >= 0:
+        return
+    raise ValueError(f"{fn}: {name} must be a contiguous {' or '.join(str(d) for d in dtypes)} tensor of shape "
+                     f"{tuple(shape)} on {'the CUDA device of the others' if dev >= 0 else 'a CUDA device'}; got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _cuda_device(fn, t):
-    if t.device.type != "cuda":
-        raise ValueError(f"{fn}: the operands must be CUDA tensors; got one on {t.device}")
-    return t.device
+def _two_dims(fn, name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{fn}: {name} must have two dimensions; got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _launch(dev, stream, call):
+    """call(raw stream) with CUDA device `dev` current."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(dev, stream, call)
+    # (torch.cuda.current_stream() builds a Stream object: 3 us of a small call)
+    return call(torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+
+
+def _empty(shape, dtype, dev, stream):
+    """An output or scratch buffer from the pool of the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
 
 
 def i8_quantize(X, Q=None, scale=None, stream=None):
     """bf16 rows X [M][K] -> (int8 codes [M][K], fp32 scales [M]); see include/q4k.h."""
-    dev = _cuda_device("i8_quantize", X)
-    if X.dim() != 2:
-        raise ValueError(f"i8_quantize: X must have two dimensions; got shape {tuple(X.shape)}")
-    M, K = X.shape
-    _need("i8_quantize", "X", X, _BF16, (M, K), dev)
-    on = _On(dev, stream)
-    with on as st:
-        if Q is None:
-            Q = on.empty((M, K), torch.int8)
-        else:
-            _need("i8_quantize", "Q", Q, _I8, (M, K), dev)
-        if scale is None:
-            scale = on.empty((M,), torch.float32)
-        else:
-            _need("i8_quantize", "scale", scale, _F32, (M,), dev)
-        _check("i8_quantize", lib().i8_quantize(X.data_ptr(), M, K, Q.data_ptr(), scale.data_ptr(), st))
+    fn, dev = "i8_quantize", X.get_device()
+    shape = M, K = _two_dims(fn, "X", X)
+    _need(fn, "X", X, _BF16, shape, dev)
+    if Q is None:
+        Q = _empty((M, K), torch.int8, dev, stream)
+    else:
+        _need(fn, "Q", Q, _I8, shape, dev)
+    if scale is None:
+        scale = _empty((M,), torch.float32, dev, stream)
+    else:
+        _need(fn, "scale", scale, _F32, (M,), dev)
+    args = X.data_ptr(), M, K, Q.data_ptr(), scale.data_ptr()
+    _check(fn, _launch(dev, stream, lambda s: lib().i8_quantize(*args, s)))
     return Q, scale
 
 
@@ -427,26 +417,22 @@ def i8_gemm(W, w_scale, X, x_scale, act: int = ACT_NONE, out_bf16: bool = False,
     """Y[m][n] = x_scale[m] * w_scale[n] * (X[m] . W[n]) from int8 W [N][K] and X [M][K];
     fp32, or bf16 with out_bf16 (or a bf16 Y). ACT_SWIGLU: bf16 [M][N/2], SiLU of the first
     N/2 channels times the others."""
-    dev = _cuda_device("i8_gemm", W)
-    if W.dim() != 2 or X.dim() != 2:
-        raise ValueError(f"i8_gemm: W and X must have two dimensions; got {tuple(W.shape)}, {tuple(X.shape)}")
-    N, K = W.shape
-    M = X.shape[0]
-    _need("i8_gemm", "W", W, _I8, (N, K), dev)
-    _need("i8_gemm", "w_scale", w_scale, _F32, (N,), dev)
-    _need("i8_gemm", "X", X, _I8, (M, K), dev)
-    _need("i8_gemm", "x_scale", x_scale, _F32, (M,), dev)
+    fn, dev = "i8_gemm", W.get_device()
+    N, K = _two_dims(fn, "W", W)
+    M = _two_dims(fn, "X", X)[0]
+    _need(fn, "W", W, _I8, (N, K), dev)
+    _need(fn, "w_scale", w_scale, _F32, (N,), dev)
+    _need(fn, "X", X, _I8, (M, K), dev)
+    _need(fn, "x_scale", x_scale, _F32, (M,), dev)
     swiglu = act == ACT_SWIGLU
-    on = _On(dev, stream)
-    with on as st:
-        shape = (M, N // 2 if swiglu else N)
-        if Y is None:
-            Y = on.empty(shape, torch.bfloat16 if swiglu or out_bf16 else torch.float32)
-        else:
-            _need("i8_gemm", "Y", Y, (torch.bfloat16,) if swiglu or out_bf16 else (torch.float32, torch.bfloat16),
-                  shape, dev)
-        _check("i8_gemm", lib().i8_gemm(W.data_ptr(), w_scale.data_ptr(), X.data_ptr(), x_scale.data_ptr(),
-                                        Y.data_ptr(), M, N, K, act, int(Y.dtype == torch.bfloat16), st))
+    shape = (M, N // 2 if swiglu else N)
+    if Y is None:
+        Y = _empty(shape, torch.bfloat16 if swiglu or out_bf16 else torch.float32, dev, stream)
+    else:
+        _need(fn, "Y", Y, (torch.bfloat16,) if swiglu or out_bf16 else (torch.float32, torch.bfloat16), shape, dev)
+    args = (W.data_ptr(), w_scale.data_ptr(), X.data_ptr(), x_scale.data_ptr(), Y.data_ptr(), M, N, K, act,
+            Y.dtype == torch.bfloat16)
+    _check(fn, _launch(dev, stream, lambda s: lib().i8_gemm(*args, s)))
     return Y
 
 
@@ -455,12 +441,10 @@ def moe_i8_layer(logits, topk: int, W_gate_up, s_gate_up, W_down, s_down, X, res
     """A whole mixture-of-experts layer for up to 32 tokens over int8 experts, in two launches
     (see include/q4k.h): logits fp32 [M][E], W_gate_up int8 [E][2F][H], W_down int8 [E][H][F]
     with fp32 scales [E][2F] and [E][H], X bf16 [M][H]; returns Y fp32 [M][H]."""
-    fn = "moe_i8_layer"
-    dev = _cuda_device(fn, W_gate_up)
-    if logits.dim() != 2 or W_down.dim() != 3:
-        raise ValueError(f"{fn}: logits must have two dimensions and W_down three; got {tuple(logits.shape)}, "
-                         f"{tuple(W_down.shape)}")
-    M, E = logits.shape
+    fn, dev = "moe_i8_layer", W_gate_up.get_device()
+    M, E = _two_dims(fn, "logits", logits)
+    if W_down.dim() != 3:
+        raise ValueError(f"{fn}: W_down must have three dimensions; got shape {tuple(W_down.shape)}")
     _, H, F = W_down.shape
     _need(fn, "logits", logits, _F32, (M, E), dev)
     _need(fn, "W_gate_up", W_gate_up, _I8, (E, 2 * F, H), dev)
@@ -470,20 +454,18 @@ def moe_i8_layer(logits, topk: int, W_gate_up, s_gate_up, W_down, s_down, X, res
     _need(fn, "X", X, _BF16, (M, H), dev)
     if residual is not None:
         _need(fn, "residual", residual, _F32, (M, H), dev)
-    on = _On(dev, stream)
-    with on as st:
-        if Y is None:
-            Y = on.empty((M, H), torch.float32)
-        else:
-            _need(fn, "Y", Y, _F32, (M, H), dev)
-        if ws is None:
-            ws = on.empty((max(16, q4k_workspace_bytes(OP_MOE_I8, M, H, F, E, topk)),), torch.uint8)
-        elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev:
-            raise ValueError(f"{fn}: ws must be a contiguous torch.uint8 tensor on {dev}")
-        _check(fn, lib().moe_i8_layer(logits.data_ptr(), M, E, topk, W_gate_up.data_ptr(), s_gate_up.data_ptr(),
-                                      W_down.data_ptr(), s_down.data_ptr(), H, F, X.data_ptr(),
-                                      None if residual is None else residual.data_ptr(), Y.data_ptr(),
-                                      ws.data_ptr(), ws.numel(), st))
+    if Y is None:
+        Y = _empty((M, H), torch.float32, dev, stream)
+    else:
+        _need(fn, "Y", Y, _F32, (M, H), dev)
+    if ws is None:
+        ws = _empty((max(16, q4k_workspace_bytes(OP_MOE_I8, M, H, F, E, topk)),), torch.uint8, dev, stream)
+    else:
+        _need(fn, "ws", ws, (torch.uint8,), (ws.numel(),), dev)
+    args = (logits.data_ptr(), M, E, topk, W_gate_up.data_ptr(), s_gate_up.data_ptr(), W_down.data_ptr(),
+            s_down.data_ptr(), H, F, X.data_ptr(), None if residual is None else residual.data_ptr(), Y.data_ptr(),
+            ws.data_ptr(), ws.numel())
+    _check(fn, _launch(dev, stream, lambda s: lib().moe_i8_layer(*args, s)))
     return Y
 
 
