@@ -3,35 +3,47 @@
 //
 //   amax = max_k |x_k|,  scale = RN_fp32(amax / 127),  q_k = RNE(127 x_k / amax)
 //
-// The code is the exact quotient rounded to nearest, ties to even: 127 x has 15
-// significant bits, so the remainder 127 x - q amax of a candidate q is exact in fp32 and
-// settles what a rounded reciprocal leaves open next to a tie. A row of zeros gets scale 0
-// and codes 0; a row that holds an infinity or a NaN gets scale NaN and codes 0, so that
-// every product with it is NaN.
+// The code is the exact quotient rounded to nearest, ties to even. A quotient rounded to 24
+// bits decides that as well as the exact one: 127 x has 15 significant bits and amax 8, so a
+// quotient that is not half an odd number is at least 2^-17 of one away, and half odd
+// numbers below 128 are representable. (Ties are common: one value in a few hundred.)
+// A row of zeros gets scale 0 and codes 0; a row that holds an infinity or a NaN gets scale
+// NaN and codes 0, so that every product with it is NaN.
 #pragma once
 #include "common.cuh"
 
 namespace q4k {
 
-constexpr int kI8QVec = 4;  // 8-value pieces of a row that a thread keeps in registers
-
-// Code of x, given amax > 0 and inv = RN(127 / amax), all three scaled by the same power
-// of two so that 127 x does not overflow.
-__device__ __forceinline__ int i8_code(float x, float amax, float inv) {
-  float q = rintf(x * inv);
-  const float rem = fmaf(-q, amax, 127.f * x);  // exact
-  const float twice = fabsf(rem) * 2.f;
-  if (twice >= amax) {  // next to or on a tie: rare
-    const float step = rem > 0.f ? 1.f : -1.f;
-    if (twice > amax || ((int)q & 1)) q += step;
-  }
-  return (int)q;
+__device__ __forceinline__ float i8_bf16_at(const uint32_t (&w)[4], int i) {
+  return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
 }
 
-// TPR threads per row, 32 .. 1024 (several rows per CTA at 32). The row stays in registers
-// between the maximum and the codes when it has at most TPR * 8 * kI8QVec values; the rest
-// of a longer one is read again.
-template <int TPR>
+// Codes of eight values, amax and rcp = RN(1 / amax) given, SCALED: the values times `two`
+// first. The quotient by one residual step: t is within 2 ulp of it, 127 x - t amax is exact,
+// and the corrected t rounds correctly; adding 1.5 * 2^23 rounds it to the integer that the
+// sum's low byte holds.
+template <bool SCALED>
+__device__ __forceinline__ uint2 i8_codes(const uint4& a, float amax, float rcp, float two) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  uint32_t m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = 127.f * (SCALED ? i8_bf16_at(w, i) * two : i8_bf16_at(w, i));  // exact
+    const float t = x * rcp;
+    m[i] = __float_as_uint(fmaf(fmaf(-t, amax, x), rcp, t) + 12582912.f);
+  }
+  uint2 o;
+  o.x = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
+  o.y = __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410);
+  return o;
+}
+
+// TPR threads per row, 32 .. 1024 (several rows per CTA below 256). The row stays in
+// registers between the maximum and the codes when it has at most TPR * 8 * V values; the
+// rest of a longer one is read again. Bound by DRAM (3 bytes a value); what counts is few
+// instructions per value: with a division's remainder checked for each, the 4096 x 5120
+// case took 18.4 us instead of {T}.
+template <int TPR, int V>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 i8_quantize_kernel(const uint16_t* __restrict__ X, int M, int K, int8_t* __restrict__ Q, float* __restrict__ scale) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -45,22 +57,21 @@ i8_quantize_kernel(const uint16_t* __restrict__ X, int M, int K, int8_t* __restr
   const bool live = row < M;
   const int nv = K / 8;
   const uint16_t* x = X + (live ? row : 0) * K;
-  uint4 v[kI8QVec];
+  uint4 v[V];
   uint32_t m = 0;
   auto take = [&](const uint4& a) {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    m = __vmaxu2(__vmaxu2(m, __vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu)),
+                 __vmaxu2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
   };
 #pragma unroll
-  for (int i = 0; i < kI8QVec; ++i) {
+  for (int i = 0; i < V; ++i) {
     const int p = t + i * TPR;
     v[i] = live && p < nv ? ldg_stream_u4(x + 8 * (int64_t)p) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
-  for (int i = 0; i < kI8QVec; ++i) take(v[i]);
+  for (int i = 0; i < V; ++i) take(v[i]);
   if (live)
-    for (int p = t + kI8QVec * TPR; p < nv; p += TPR) take(ldg_u4(x + 8 * (int64_t)p));
+    for (int p = t + V * TPR; p < nv; p += TPR) take(ldg_u4(x + 8 * (int64_t)p));
   uint32_t mb = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));  // bits of amax
   if constexpr (kWarps > 1) {
     __shared__ uint32_t part[kThreads / 32];
@@ -74,29 +85,28 @@ i8_quantize_kernel(const uint16_t* __restrict__ X, int M, int K, int8_t* __restr
   const bool good = mb < 0x7F80u;
   float amax = bf16_bits_to_float(mb);
   if (t == 0) scale[row] = good ? amax / 127.f : __uint_as_float(0x7FC00000u);
-  // the same power of two on x and amax: 127 x stays in range and 127 / amax is normal
-  const float two = mb >= 0x7180u ? 0x1p-64f : (mb < 0x2000u ? 0x1p64f : 1.f);
-  amax *= two;
-  const float inv = good && mb ? 127.f / amax : 0.f;
   int8_t* q = Q + row * K;
-  auto put = [&](int p, const uint4& a) {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-    uint32_t o[2] = {0u, 0u};
-    if (good && mb) {
+  auto each = [&](auto&& codes) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float xv = bf16_bits_to_float(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu) * two;
-        o[i >> 2] |= ((uint32_t)i8_code(xv, amax, inv) & 0xFFu) << (8 * (i & 3));
-      }
+    for (int i = 0; i < V; ++i) {
+      const int p = t + i * TPR;
+      if (p < nv) *reinterpret_cast<uint2*>(q + 8 * (int64_t)p) = codes(v[i]);
     }
-    *reinterpret_cast<uint2*>(q + 8 * (int64_t)p) = make_uint2(o[0], o[1]);
+    for (int p = t + V * TPR; p < nv; p += TPR)
+      *reinterpret_cast<uint2*>(q + 8 * (int64_t)p) = codes(ldg_u4(x + 8 * (int64_t)p));
   };
-#pragma unroll
-  for (int i = 0; i < kI8QVec; ++i) {
-    const int p = t + i * TPR;
-    if (p < nv) put(p, v[i]);
+  if (!good || mb == 0) {
+    each([](const uint4&) { return make_uint2(0u, 0u); });
+  } else if (mb >= 0x7180u || mb < 0x2000u) {
+    // 127 x would overflow, or 1 / amax not be normal: all times a power of two first
+    const float two = mb >= 0x7180u ? 0x1p-64f : 0x1p64f;
+    amax *= two;
+    const float rcp = 1.f / amax;
+    each([&](const uint4& a) { return i8_codes<true>(a, amax, rcp, two); });
+  } else {
+    const float rcp = 1.f / amax;
+    each([&](const uint4& a) { return i8_codes<false>(a, amax, rcp, 1.f); });
   }
-  for (int p = t + kI8QVec * TPR; p < nv; p += TPR) put(p, ldg_u4(x + 8 * (int64_t)p));
 }
 
 }  // namespace q4k

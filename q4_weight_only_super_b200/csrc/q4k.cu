@@ -892,13 +892,12 @@ q4k_status i8_quantize(const uint16_t* X, int M, int K, int8_t* Q, float* scale,
   if (!aligned16(X) || !aligned16(Q) || !aligned16(scale)) return Q4K_ERR_ALIGN;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto rows = [&](int per) { return dim3((unsigned)((M + (int64_t)per - 1) / per)); };
-  // the fewest threads that hold a row in registers: more rows in flight per SM
-  constexpr int kHold = 8 * kI8QVec;
-  if (K <= 32 * kHold) return launch_pdl(i8_quantize_kernel<32>, rows(8), dim3(256), s, X, M, K, Q, scale);
-  if (K <= 128 * kHold) return launch_pdl(i8_quantize_kernel<128>, rows(2), dim3(256), s, X, M, K, Q, scale);
-  if (K <= 256 * kHold) return launch_pdl(i8_quantize_kernel<256>, rows(1), dim3(256), s, X, M, K, Q, scale);
-  if (K <= 512 * kHold) return launch_pdl(i8_quantize_kernel<512>, rows(1), dim3(512), s, X, M, K, Q, scale);
-  return launch_pdl(i8_quantize_kernel<1024>, rows(1), dim3(1024), s, X, M, K, Q, scale);
+  // the fewest threads that hold a row in registers, for more rows in flight per SM
+  if (K <= 32 * 8 * 4) return launch_pdl(i8_quantize_kernel<32, 4>, rows(8), dim3(256), s, X, M, K, Q, scale);
+  if (K <= 128 * 8 * 5) return launch_pdl(i8_quantize_kernel<128, 5>, rows(2), dim3(256), s, X, M, K, Q, scale);
+  if (K <= 256 * 8 * 5) return launch_pdl(i8_quantize_kernel<256, 5>, rows(1), dim3(256), s, X, M, K, Q, scale);
+  if (K <= 512 * 8 * 5) return launch_pdl(i8_quantize_kernel<512, 5>, rows(1), dim3(512), s, X, M, K, Q, scale);
+  return launch_pdl(i8_quantize_kernel<1024, 4>, rows(1), dim3(1024), s, X, M, K, Q, scale);
 }
 
 q4k_status i8_gemm(const int8_t* W, const float* w_scale, const int8_t* X, const float* x_scale, void* Y, int M, int N,
