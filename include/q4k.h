@@ -366,13 +366,13 @@ q4k_status i8_gemm(const int8_t* W, const float* w_scale, const int8_t* X, const
  *     h = SiLU(g) * u, g and u = s_gate_up * (W_gate_up[e] X[t]).
  * No 8-bit rounding inside: X and h (fp32) enter the integer products as 24-bit fixed
  * point with one scale per row (X: a power of two, so a value within 2^14 of its row's
- * largest is exact; h: to 2^-23 of its row's largest), the products' sums are exact, and
+ * largest is exact; h: to 2^-23 of its row's largest, or of 2^-100), their sums exact, and
  * the combine is summed in fp32 in an order that depends on the sizes and the routing
  * alone. A token whose X holds an infinity or a NaN gets NaN.
  *   ws/ws_bytes: device scratch of q4k_workspace_bytes(Q4K_OP_MOE_I8, M, H, F, E, topk)
  *   bytes; calls (and captured graphs) that share it must be ordered on one stream.
- * H % 16 == 0, F % 16 == 0, both <= 131056, E * max(2F, H) < 2^31 - 256; E <= 1024,
- * topk <= min(E, 16). M == 0 is a no-op. */
+ * H % 16 == 0, F % 16 == 0, both <= 131056; E <= 1024, topk <= min(E, 16). M == 0 is
+ * a no-op. */
 q4k_status moe_i8_layer(const float* logits, int M, int E, int topk, const int8_t* W_gate_up, const float* s_gate_up,
                         const int8_t* W_down, const float* s_down, int H, int F, const uint16_t* X,
                         const float* residual, float* Y, void* ws, size_t ws_bytes, void* stream);

@@ -5,4 +5,4 @@ Only ``tests/``, ``__graft_entry__.smoke()`` and the CPU-baseline leg of
 under ``q4_weight_only_super_b200/`` and its binding) never imports, links or
 runs anything here, and the two share no code.
 """
-from . import q4k  # noqa: F401
+from . import i8, q4k  # noqa: F401

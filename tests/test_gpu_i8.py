@@ -230,12 +230,13 @@ def route_ref(logits, topk):
 
 
 def moe_ref(L, topk, Wg, sg, Wd, sd, X, residual=None):
-    """(value, sum of magnitudes of its terms) per output, in 64 bits."""
+    """(value, sum of magnitudes of its terms, sum of the down weights' magnitudes) per output, in
+    64 bits."""
     M, E = L.shape
     F, H = Wd.shape[2], Wd.shape[1]
     ids, ws = route_ref(L, topk)
     y = torch.zeros(M, H, dtype=F64, device="cuda") if residual is None else residual.to(F64).clone()
-    S = y.abs().clone()
+    S, A = y.abs().clone(), torch.zeros_like(y)
     for t in range(M):
         x = X[t].to(F64)
         for e, p in zip(ids[t], ws[t]):
@@ -249,7 +250,8 @@ def moe_ref(L, topk, Wg, sg, Wd, sd, X, residual=None):
             hm = 1.1 * a[:F] * up.abs() + a[F:] * (gate * sig).abs() + h.abs()
             y[t] += p * (wd @ h)
             S[t] += p * (wd.abs() @ hm)
-    return y, S
+            A[t] += p * wd.abs().sum(1)
+    return y, S, A
 
 
 def moe_inputs(seed, M, E, H, F):
@@ -262,12 +264,13 @@ def moe_inputs(seed, M, E, H, F):
 
 
 def check_moe(Y, L, topk, Wg, sg, Wd, sd, X, residual=None):
-    y, S = moe_ref(L, topk, Wg, sg, Wd, sd, X, residual)
+    y, S, A = moe_ref(L, topk, Wg, sg, Wd, sd, X, residual)
     H, F = X.shape[1], Wd.shape[2]
     # fp32 sums of exact products: at most one rounding (2^-23, truncation allowed for) per
     # 16-term MMA step and per later addition, of a partial sum below the sum of magnitudes
     u = 2.0 ** -23
     tol = ((H / 16 + F / 16 * 3 + 64 + topk) * u + 1e-6) * S  # 1e-6: the routing weights' own bound
+    tol += 2.0 ** -123 * A  # the resolution of h where it is below 2^-100 throughout a row
     err = (Y.to(F64) - y).abs()
     assert (err <= tol).all(), float((err / tol.clamp_min(1e-300)).max())
 
