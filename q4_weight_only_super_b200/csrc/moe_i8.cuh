@@ -358,8 +358,12 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   const int tiles = (p.F + 63) / 64;  // kernel 1
   const int first = DOWN ? (int)(blockIdx.x % (unsigned)p.split) : (int)blockIdx.x;
   const int col0 = DOWN ? (int)(blockIdx.x / (unsigned)p.split) * kI8Rows : 0;  // (past H: a spare CTA of the last cluster)
-  const int units = DOWN ? (col0 < p.H ? r.groups : 0) : r.groups * tiles;
-  const int step = DOWN ? p.split : (int)gridDim.x;
+  int units = DOWN ? (col0 < p.H ? r.groups : 0) : r.groups * tiles;
+  // Kernel 1 leaves CTAs out so that all finish in the same round: DRAM bounds it, and a last
+  // round of a few CTAs would wait for their latency (3 us at 8 and at 32 tokens).
+  const int grid = (int)gridDim.x, rounds = (units + grid - 1) / grid;
+  const int step = DOWN ? p.split : (units + max(rounds, 1) - 1) / max(rounds, 1);
+  if (!DOWN && first >= step) units = 0;
   auto group_of = [&](int u) { return DOWN ? u : u / tiles; };
   // scale of row j of a group that starts at row0
   auto row_scale = [&](int row0, int j) { return s_scale[DOWN ? row0 + j : r.row_token[row0 + j]]; };

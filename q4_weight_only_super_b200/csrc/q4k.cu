@@ -500,22 +500,24 @@ I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
   const double dram = ((double)rows * (kI8Rows / tile_rows) + M) * K / 2250.;
   I8Cut best = {};
   double least = 1e300;
-  for (int form = 0; form < 3; ++form) {  // lone CTAs, two lone CTAs per SM, pairs
-    const int pair = form == 2, P = pair + 1, grain = 16 * P;
+  for (int form = 0; form < 4; ++form) {  // lone CTAs or pairs, one CTA per SM or two
+    const int pair = form >> 1, P = pair + 1, grain = 16 * P;
     const int fewest = (M + kI8MaxNT - 1) / kI8MaxNT;
     for (int mt = fewest; mt < fewest + 3; ++mt) {
       I8Cut c = {};
       c.pair = pair;
-      c.halved = form == 1;
+      c.halved = form & 1;
       c.m_tiles = mt;
       c.nt = ((M + mt - 1) / mt + grain - 1) / grain * grain;
-      if (c.nt > kI8MaxNT || (c.halved && c.nt > kI8MaxNT / 2)) continue;
+      if (c.nt > kI8MaxNT) continue;
       c.n_tiles = (rows + tile_rows * P - 1) / (tile_rows * P);
       const size_t stage = kI8ATile + (size_t)(c.nt / P) * kI8KB;
       c.stages = std::min<int>(kI8MaxStages, (int)((kI8Smem[c.halved] - 1024 - kI8TailBytes) / stage));
       const double tiles = (double)c.n_tiles * mt;
       const double work = std::max(1.48 * c.nt, stage / 108.), ring = 1140. / std::min(c.stages, 3);
       for (int ks = 1; ks <= std::min(8 / P, nk); ++ks) {
+        // two CTAs share an SM's 512 TMEM columns, and a CTA that walks tiles has two accumulators
+        if (c.halved && (ks > 1 ? 1 : 2) * c.nt > 256) continue;
         c.ksplit = ks;
         const double ctas = tiles * P * ks;
         if (ks > 1) {
