@@ -188,7 +188,7 @@ __device__ __forceinline__ int i8_row(int n_tile, int q, int lane, bool* up) {
 __host__ __device__ __forceinline__ int i8_part_pitch(int per) { return per / 4 % 2 ? per : per + 4; }
 
 template <bool SWIGLU, bool BF16, bool PAIR, bool SPLIT>
-__global__ void __launch_bounds__(kI8Threads)
+__global__ void __launch_bounds__(kI8Threads, 2)
 i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x, I8GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);

@@ -193,26 +193,9 @@ __device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r, f
   uint64_t* list = reinterpret_cast<uint64_t*>(scratch) + warp * 32 * PL;
 #pragma unroll 1
   for (int t = rank + kMi8Cluster * warp; t < p.M; t += kMi8Cluster * kMi8Warps) {
-    float logit[PL];
-#pragma unroll
-    for (int j = 0; j < PL; ++j) logit[j] = 32 * j + lane < p.E ? p.logits[(int64_t)t * p.E + 32 * j + lane] : 0.f;
-    if (SCALES) {
-      uint32_t m = 0;
-#pragma unroll 8
-      for (int k = 8 * lane; k < p.H; k += 256) {
-        const uint4 x = ldg_u4(p.X + (int64_t)t * p.H + k);
-        m = __vmaxu2(__vmaxu2(m, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)),
-                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
-      }
-      const float2 sc = mi8_scale<true>(__reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)) << 16);
-      if (lane < kMi8Cluster) {
-        st_cluster(reinterpret_cast<uint32_t*>(&scale[t].x), lane, __float_as_uint(sc.x));
-        st_cluster(reinterpret_cast<uint32_t*>(&scale[t].y), lane, __float_as_uint(sc.y));
-      }
-    }
     uint32_t key[PL];
 #pragma unroll
-    for (int j = 0; j < PL; ++j) key[j] = 32 * j + lane < p.E ? mi8_key(logit[j]) : 0u;
+    for (int j = 0; j < PL; ++j) key[j] = 32 * j + lane < p.E ? mi8_key(p.logits[(int64_t)t * p.E + 32 * j + lane]) : 0u;
     uint16_t* id = r.id + t * p.topk;
     uint32_t* w = r.w + t * p.topk;
     mi8_topk<PL>(key, p.topk, lane, list, id, w);
@@ -231,6 +214,23 @@ __device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r, f
         st_cluster(id + lane, c, e);
         st_cluster(w + lane, c, __float_as_uint(ek / den));
         or_cluster(&r.tmask[e], c, 1u << t);
+      }
+    }
+  }
+  if (SCALES) {  // by other warps than route the tokens, as far as there are
+#pragma unroll 1
+    for (int t = rank + kMi8Cluster * ((warp + kMi8Warps / 2) % kMi8Warps); t < p.M; t += kMi8Cluster * kMi8Warps) {
+      uint32_t m = 0;
+#pragma unroll 8
+      for (int k = 8 * lane; k < p.H; k += 256) {
+        const uint4 x = ldg_u4(p.X + (int64_t)t * p.H + k);
+        m = __vmaxu2(__vmaxu2(m, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)),
+                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+      }
+      const float2 sc = mi8_scale<true>(__reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)) << 16);
+      if (lane < kMi8Cluster) {
+        st_cluster(reinterpret_cast<uint32_t*>(&scale[t].x), lane, __float_as_uint(sc.x));
+        st_cluster(reinterpret_cast<uint32_t*>(&scale[t].y), lane, __float_as_uint(sc.y));
       }
     }
   }
@@ -286,8 +286,20 @@ __device__ __forceinline__ void mi8_digits(const float (&x)[4], float S, uint32_
   d[0] = __byte_perm(__byte_perm(v[0], v[1], 0x0062), __byte_perm(v[2], v[3], 0x0062), 0x5410);
 }
 
+// Four floats from L2, or zeros (volatile: the loads of a batch stay together, ahead of the
+// first sum).
+__device__ __forceinline__ float4 mi8_ldcg_if(const float* p, bool in) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n @p ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n}"
+      : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w)
+      : "l"(p), "r"((int)in)
+      : "memory");
+  return v;
+}
+
 template <int PL, bool DOWN>
-__global__ void __launch_bounds__(32 * kMi8Warps)
+__global__ void __launch_bounds__(32 * kMi8Warps, 2)
 mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Mi8Route<PL> r;
@@ -584,10 +596,14 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
       if (p.split == 1) {
         y = *reinterpret_cast<const float4*>(ysum + i);
       } else {
-#pragma unroll 4
-        for (int q = 0; q < p.split; ++q) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + ((int64_t)tile * p.split + q) * n + i));
-          y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+        // (16 in flight at once: four at a time the last CTA took 8 us for 32 tokens)
+        for (int q0 = 0; q0 < p.split; q0 += 16) {
+          float4 v[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            v[q] = mi8_ldcg_if(p.part + ((int64_t)tile * p.split + q0 + q) * n + i, q0 + q < p.split);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) y.x += v[q].x, y.y += v[q].y, y.z += v[q].z, y.w += v[q].w;
         }
       }
       const int64_t at = (int64_t)t * p.H + c;  // (H % 16 == 0: four columns are in or out together)
