@@ -489,15 +489,16 @@ struct I8Cut {
 };
 
 // The cut with the least estimated time, in SM cycles. A stage (128 bytes of K of a CTA's
-// tiles) takes 1.48 cycles a token for the MMAs, or its bytes at 108 a cycle from L2, and
-// not less than the ring's latency allows; weights and tokens come from DRAM at 2250 bytes a
+// tiles) takes 1.18 cycles a token for the MMAs, or its bytes at 111 a cycle from L2, and
+// not less than the ring's latency allows; weights and tokens come from DRAM at 2380 bytes a
 // cycle; the smaller of the two is not hidden by the larger altogether; a K split pays for
 // its exchange, a pair for its hand-shakes. The constants are fitted to 29 shapes (1 .. 3000
-// tokens, 200 .. 34816 channels, K 512 .. 17408), every cut of each measured: the chosen one
-// is 1.5% slower than the fastest in the mean, 18% at most (37 x 2051 x 2064: 7.3 for 6.1 us).
+// tokens, 200 .. 34816 channels, K 512 .. 17408), every cut of each measured, and mean nothing
+// beyond that: the chosen cut is 1.5% slower than the fastest in the mean, 12% at most (1500 x
+// 600 x 4096: 15.5 for 13.8 us; 37 x 2051 x 2064: 6.8 for 6.1 us).
 I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
   const int nk = (K + kI8KB - 1) / kI8KB;
-  const double dram = ((double)rows * (kI8Rows / tile_rows) + M) * K / 2250.;
+  const double dram = ((double)rows * (kI8Rows / tile_rows) + M) * K / 2380.;
   I8Cut best = {};
   double least = 1e300;
   for (int form = 0; form < 4; ++form) {  // lone CTAs or pairs, one CTA per SM or two
@@ -514,7 +515,7 @@ I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
       const size_t stage = kI8ATile + (size_t)(c.nt / P) * kI8KB;
       c.stages = std::min<int>(kI8MaxStages, (int)((kI8Smem[c.halved] - 1024 - kI8TailBytes) / stage));
       const double tiles = (double)c.n_tiles * mt;
-      const double work = std::max(1.48 * c.nt, stage / 108.), ring = 1140. / std::min(c.stages, 3);
+      const double work = std::max(1.18 * c.nt, stage / 111.), ring = 1120. / std::min(c.stages, 3);
       for (int ks = 1; ks <= std::min(8 / P, nk); ++ks) {
         // two CTAs share an SM's 512 TMEM columns, and a CTA that walks tiles has two accumulators
         if (c.halved && (ks > 1 ? 1 : 2) * c.nt > 256) continue;
@@ -528,8 +529,8 @@ I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
         const double waves = std::ceil(ctas / (sms * (1 + c.halved)));
         const double share = c.halved && ctas > sms ? 2 : 1;
         const double mma = waves * std::ceil((double)nk / ks) * std::max(share * work, ring);
-        const double t = std::max(mma, dram) + 0.187 * std::min(mma, dram) +
-                         (ks > 1 ? 2450. + 6.7 * c.nt + 425. * ks : 2.7 * c.nt) + 350. * pair;
+        const double t = std::max(mma, dram) + 0.172 * std::min(mma, dram) +
+                         (ks > 1 ? 2615. + 5.6 * c.nt + 369. * ks : 2.6 * c.nt) + 367. * pair;
         if (t < least) {
           least = t;
           best = c;
