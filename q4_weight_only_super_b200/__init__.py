@@ -363,7 +363,7 @@ _I8, _F32 = (torch.int8,), (torch.float32,)
 
 def _need(fn, name, t, dtypes, shape, dev):
     """An operand of the int8 lane: contiguous, of the right type and shape, on CUDA device `dev`."""
-    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev >= 0:
+    if t.shape == shape and t.dtype in dtypes and t.get_device() == dev >= 0 and t.is_contiguous():
         return
     raise ValueError(f"{fn}: {name} must be a contiguous {' or '.join(str(d) for d in dtypes)} tensor of shape "
                      f"{tuple(shape)} on {'the CUDA device of the others' if dev >= 0 else 'a CUDA device'}; got "
@@ -376,13 +376,8 @@ def _two_dims(fn, name, t):
     return t.shape
 
 
-def _launch(dev, stream, call):
-    """call(raw stream) with CUDA device `dev` current."""
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _launch(dev, stream, call)
-    # (torch.cuda.current_stream() builds a Stream object: 3 us of a small call)
-    return call(torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+# (torch.cuda.current_stream() builds a Stream object: 3 us of a small call)
+_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
 
 
 def _empty(shape, dtype, dev, stream):
@@ -408,8 +403,13 @@ def i8_quantize(X, Q=None, scale=None, stream=None):
         scale = _empty((M,), torch.float32, dev, stream)
     else:
         _need(fn, "scale", scale, _F32, (M,), dev)
-    args = X.data_ptr(), M, K, Q.data_ptr(), scale.data_ptr()
-    _check(fn, _launch(dev, stream, lambda s: lib().i8_quantize(*args, s)))
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return i8_quantize(X, Q, scale, stream)
+    st = lib().i8_quantize(X.data_ptr(), M, K, Q.data_ptr(), scale.data_ptr(),
+                           _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise Q4KError(fn, st)
     return Q, scale
 
 
@@ -418,9 +418,9 @@ def i8_gemm(W, w_scale, X, x_scale, act: int = ACT_NONE, out_bf16: bool = False,
     fp32, or bf16 with out_bf16 (or a bf16 Y). ACT_SWIGLU: bf16 [M][N/2], SiLU of the first
     N/2 channels times the others."""
     fn, dev = "i8_gemm", W.get_device()
-    N, K = _two_dims(fn, "W", W)
+    shape = N, K = _two_dims(fn, "W", W)
     M = _two_dims(fn, "X", X)[0]
-    _need(fn, "W", W, _I8, (N, K), dev)
+    _need(fn, "W", W, _I8, shape, dev)
     _need(fn, "w_scale", w_scale, _F32, (N,), dev)
     _need(fn, "X", X, _I8, (M, K), dev)
     _need(fn, "x_scale", x_scale, _F32, (M,), dev)
@@ -430,9 +430,13 @@ def i8_gemm(W, w_scale, X, x_scale, act: int = ACT_NONE, out_bf16: bool = False,
         Y = _empty(shape, torch.bfloat16 if swiglu or out_bf16 else torch.float32, dev, stream)
     else:
         _need(fn, "Y", Y, (torch.bfloat16,) if swiglu or out_bf16 else (torch.float32, torch.bfloat16), shape, dev)
-    args = (W.data_ptr(), w_scale.data_ptr(), X.data_ptr(), x_scale.data_ptr(), Y.data_ptr(), M, N, K, act,
-            Y.dtype == torch.bfloat16)
-    _check(fn, _launch(dev, stream, lambda s: lib().i8_gemm(*args, s)))
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return i8_gemm(W, w_scale, X, x_scale, act, out_bf16, Y, stream)
+    st = lib().i8_gemm(W.data_ptr(), w_scale.data_ptr(), X.data_ptr(), x_scale.data_ptr(), Y.data_ptr(), M, N, K, act,
+                       Y.dtype == torch.bfloat16, _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise Q4KError(fn, st)
     return Y
 
 
@@ -462,10 +466,15 @@ def moe_i8_layer(logits, topk: int, W_gate_up, s_gate_up, W_down, s_down, X, res
         ws = _empty((max(16, q4k_workspace_bytes(OP_MOE_I8, M, H, F, E, topk)),), torch.uint8, dev, stream)
     else:
         _need(fn, "ws", ws, (torch.uint8,), (ws.numel(),), dev)
-    args = (logits.data_ptr(), M, E, topk, W_gate_up.data_ptr(), s_gate_up.data_ptr(), W_down.data_ptr(),
-            s_down.data_ptr(), H, F, X.data_ptr(), None if residual is None else residual.data_ptr(), Y.data_ptr(),
-            ws.data_ptr(), ws.numel())
-    _check(fn, _launch(dev, stream, lambda s: lib().moe_i8_layer(*args, s)))
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return moe_i8_layer(logits, topk, W_gate_up, s_gate_up, W_down, s_down, X, residual, Y, ws, stream)
+    st = lib().moe_i8_layer(logits.data_ptr(), M, E, topk, W_gate_up.data_ptr(), s_gate_up.data_ptr(),
+                            W_down.data_ptr(), s_down.data_ptr(), H, F, X.data_ptr(),
+                            None if residual is None else residual.data_ptr(), Y.data_ptr(), ws.data_ptr(),
+                            ws.numel(), _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise Q4KError(fn, st)
     return Y
 
 
