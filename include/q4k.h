@@ -349,7 +349,8 @@ q4k_status i8_quantize(const uint16_t* X, int M, int K, int8_t* Q, float* scale,
  *   act == Q4K_ACT_SWIGLU: Y bf16 [M][N/2] (out_bf16 must be set), SiLU(g) * u with
  *     g = y of rows 0..N/2-1 of W, u = y of rows N/2..N-1.
  * The sums are exact, so a result does not depend on the batch or the launch shape.
- * K <= 131056 (the sums fit int32); any N. M == 0 or N == 0 is a no-op. */
+ * K <= 131056 (the sums fit int32); M and N up to 2^31 - 1024. M == 0 or N == 0 is a
+ * no-op. */
 q4k_status i8_gemm(const int8_t* W, const float* w_scale, const int8_t* X, const float* x_scale, void* Y, int M, int N,
                    int K, int act, int out_bf16, void* stream);
 

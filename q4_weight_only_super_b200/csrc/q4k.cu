@@ -577,7 +577,7 @@ q4k_status i8_gemm_t(const int8_t* W, const int8_t* X, I8GemmParams p, cudaStrea
   const int sms = sm_count();
   if (sms <= 0) return Q4K_ERR_CUDA;
   const int rows = SWIGLU ? p.N / 2 : p.N, tile_rows = SWIGLU ? kI8Rows / 2 : kI8Rows;
-  if (((int64_t)rows / tile_rows + 2) * (p.M / 16 + 4) > 0x7fffffffLL / 16) return Q4K_ERR_UNSUPPORTED;
+  if (((int64_t)rows / tile_rows + 2) * (p.M / kI8MaxNT + 4) > 0x7fffffffLL / 16) return Q4K_ERR_UNSUPPORTED;
   const I8Cut& c = i8_cut_of(p.M, rows, tile_rows, p.K, sms);
   p.nt = c.nt;
   p.n_tiles = c.n_tiles;
@@ -912,7 +912,9 @@ q4k_status i8_gemm(const int8_t* W, const float* w_scale, const int8_t* X, const
   if (!W || !w_scale || !X || !x_scale || !Y) return Q4K_ERR_NULL;
   if (!aligned16(W) || !aligned16(w_scale) || !aligned16(X) || !aligned16(x_scale) || !aligned16(Y))
     return Q4K_ERR_ALIGN;
-  if (K > kI8MaxK || (act == Q4K_ACT_SWIGLU && !out_bf16)) return Q4K_ERR_UNSUPPORTED;
+  // the sums, and the tiles' first rows, fit int32
+  if (K > kI8MaxK || M > kI8MaxRows || N > kI8MaxRows || (act == Q4K_ACT_SWIGLU && !out_bf16))
+    return Q4K_ERR_UNSUPPORTED;
   I8GemmParams p = {};
   p.xs = x_scale;
   p.ws = w_scale;

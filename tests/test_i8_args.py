@@ -76,6 +76,7 @@ def test_gemm_refusals(L):
     assert f(act=1, N=33, bf16=1) == 3     # an odd number of gate and up rows
     assert f(act=1, bf16=0) == 4           # SwiGLU is bf16
     assert f(K=131072) == 4                # sums beyond int32
+    assert f(M=2 ** 31 - 1) == 4 and f(N=2 ** 31 - 1) == 4
     for name in ("W", "ws", "X", "xs", "Y"):
         assert f(**{name: None}) == 1
         assert f(**{name: FAKE + 4}) == 2
