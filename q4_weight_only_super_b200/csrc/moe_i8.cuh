@@ -30,9 +30,9 @@
 // of the epilogue, one shuffle brings a pair together); units go round-robin over the CTAs.
 // h leaves as fp32 with the largest magnitude of every 16 of a row. Kernel 2: a CTA owns
 // 128 output columns and every split-th expert: the weighted rows are summed in shared
-// memory, and the last CTA of a column tile to finish adds the splits' sums in their order
-// (a counter, but no atomics on results: deterministic).
-// Both kernels know the whole routing: each cluster of four CTAs routes the tokens, a warp
+// memory, and the CTAs of a column tile, one cluster's, add theirs in a fixed order through
+// distributed shared memory (no atomics on results: deterministic).
+// Both kernels know the whole routing: each cluster routes the tokens, a warp
 // per token, and shares what it finds; kernel 2 then starts its weight stream before kernel
 // 1 has ended (programmatic dependent launch) and waits for it only before it reads h.
 // Every wait is bounded; on expiry the kernel latches Q4K_ERR_DEVICE_TIMEOUT, stops all
@@ -49,7 +49,7 @@ constexpr int kMi8MaxM = 32;
 constexpr int kMi8MaxRows = kMi8MaxM * kMaxTopk;  // (token, slot) pairs
 constexpr int kMi8Warps = 10;
 constexpr int kMi8DigitWarps = 4;
-constexpr int kMi8Cluster = 4;    // CTAs that share the routing
+constexpr int kMi8Cluster[2] = {4, 8};  // CTAs of a cluster, which share the routing (kernel 1, 2)
 constexpr int kMi8GroupRows = 8;  // rows of a group at most
 constexpr int kMi8MaxStages = 10;
 constexpr float kMi8Top = 8355711.f;  // 127 * 65536 + 127 * 256 + 127: the largest three digits hold
@@ -63,26 +63,19 @@ struct Mi8Params {
   float* Y;
   float* h;        // [rows][F], rows sorted by (expert, token)
   uint32_t* hmax;  // [rows][hparts]: bits of the largest |h| of each 16
-  float* part;     // kernel 2: [column tile][split][M][128]
-  int32_t* count;  // kernel 2: [column tile], splits that have arrived
   int M, E, topk, H, F;
   int hparts;  // 4 per tile of kernel 1
   int nb;      // columns that a stage has room for: 4 per row of a group, rounded up to 16
   int stages, tstride, tmem_cols;
-  int split;   // kernel 2: CTAs that share a column tile, taking the experts in turn
+  int split;   // kernel 2: CTAs that share a column tile, taking the experts in turn: 1, 2, 4, 8
 };
 
 inline int mi8_tiles(int F) { return (F + 63) / 64; }
 
-constexpr int kMi8MaxCtas = 256;  // kernel 2: column tiles x splits, where split > 1
-
-// h, hmax, counters, partial sums
+// h, hmax
 inline size_t mi8_ws_h(int M, int topk, int F) { return (size_t)M * topk * F * 4; }
-inline size_t mi8_ws_hmax(int M, int topk, int F) { return (size_t)M * topk * 16 * (size_t)mi8_tiles(F); }
-inline size_t mi8_ws_bytes(int M, int topk, int H, int F) {
-  const size_t tiles = (size_t)(H + kI8Rows - 1) / kI8Rows;
-  return mi8_ws_h(M, topk, F) + mi8_ws_hmax(M, topk, F) + (tiles + 3) / 4 * 16 +
-         (size_t)kMi8MaxCtas * M * kI8Rows * 4;
+inline size_t mi8_ws_bytes(int M, int topk, int F) {
+  return mi8_ws_h(M, topk, F) + (size_t)M * topk * 16 * (size_t)mi8_tiles(F);
 }
 
 // Order of the logits as unsigned keys: -inf .. +inf, a NaN below them all, 0 for none.
@@ -189,13 +182,13 @@ __device__ __forceinline__ void or_cluster(unsigned* p, uint32_t rank, unsigned 
 // tokens each, a warp per token, and write what they find into each other's shared memory.
 // SCALES: also the tokens' scales into `scale`. scratch: 32 PL entries of 8 bytes per warp.
 // The masks are cleared, and that is known to the whole cluster, before.
-template <int PL, bool SCALES>
+template <int PL, int C, bool SCALES>
 __device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r, float2* scale, uint8_t* scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = (int)(blockIdx.x % kMi8Cluster);
+  const int rank = (int)(blockIdx.x % C);
   uint64_t* list = reinterpret_cast<uint64_t*>(scratch) + warp * 32 * PL;
 #pragma unroll 1
-  for (int t = rank + kMi8Cluster * warp; t < p.M; t += kMi8Cluster * kMi8Warps) {
+  for (int t = rank + C * warp; t < p.M; t += C * kMi8Warps) {
     uint32_t key[PL];
 #pragma unroll
     for (int j = 0; j < PL; ++j) key[j] = 32 * j + lane < p.E ? mi8_key(p.logits[(int64_t)t * p.E + 32 * j + lane]) : 0u;
@@ -213,7 +206,7 @@ __device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r, f
     if (lane < p.topk) {
       const uint16_t e = id[lane];
 #pragma unroll
-      for (int c = 0; c < kMi8Cluster; ++c) {
+      for (int c = 0; c < C; ++c) {
         st_cluster(id + lane, c, e);
         st_cluster(w + lane, c, __float_as_uint(ek / den));
         or_cluster(&r.tmask[e], c, 1u << t);
@@ -222,7 +215,7 @@ __device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r, f
   }
   if (SCALES) {  // by other warps than route the tokens, as far as there are
 #pragma unroll 1
-    for (int t = rank + kMi8Cluster * ((warp + kMi8Warps / 2) % kMi8Warps); t < p.M; t += kMi8Cluster * kMi8Warps) {
+    for (int t = rank + C * ((warp + kMi8Warps / 2) % kMi8Warps); t < p.M; t += C * kMi8Warps) {
       uint32_t m = 0;
 #pragma unroll 8
       for (int k = 8 * lane; k < p.H; k += 256) {
@@ -231,7 +224,7 @@ __device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r, f
                      __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
       }
       const float2 sc = mi8_scale<true>(__reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16)) << 16);
-      if (lane < kMi8Cluster) {
+      if (lane < C) {
         st_cluster(reinterpret_cast<uint32_t*>(&scale[t].x), lane, __float_as_uint(sc.x));
         st_cluster(reinterpret_cast<uint32_t*>(&scale[t].y), lane, __float_as_uint(sc.y));
       }
@@ -289,21 +282,19 @@ __device__ __forceinline__ void mi8_digits(const float (&x)[4], float S, uint32_
   d[0] = __byte_perm(__byte_perm(v[0], v[1], 0x0062), __byte_perm(v[2], v[3], 0x0062), 0x5410);
 }
 
-// Four floats from L2, or zeros (volatile: the loads of a batch stay together, ahead of the
-// first sum).
-__device__ __forceinline__ float4 mi8_ldcg_if(const float* p, bool in) {
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n @p ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n}"
-      : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w)
-      : "l"(p), "r"((int)in)
-      : "memory");
+__device__ __forceinline__ float4 ld_cluster_f4(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(map_cluster(p, rank))
+               : "memory");
   return v;
 }
 
 template <int PL, bool DOWN>
 __global__ void __launch_bounds__(32 * kMi8Warps, 2)
 mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
+  constexpr int C = kMi8Cluster[DOWN];
   extern __shared__ uint8_t smem_raw[];
   __shared__ Mi8Route<PL> r;
   __shared__ __align__(8) uint64_t bar_mem[3 * kMi8MaxStages + 4];
@@ -349,10 +340,10 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   if (!DOWN) {
     // this warp's tokens into L2 (a prefetch may precede the wait: it returns nothing, and L2
     // is where the kernel before this one writes)
-    for (int t = (int)(blockIdx.x % kMi8Cluster) + kMi8Cluster * warp; t < p.M; t += kMi8Cluster * kMi8Warps)
+    for (int t = (int)(blockIdx.x % C) + C * warp; t < p.M; t += C * kMi8Warps)
       for (int i = 32 * lane; i < p.E; i += 32 * 32)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.logits + (int64_t)t * p.E + i));
-    for (int t = (int)(blockIdx.x % kMi8Cluster) + kMi8Cluster * warp; t < p.M; t += kMi8Cluster * kMi8Warps)
+    for (int t = (int)(blockIdx.x % C) + C * warp; t < p.M; t += C * kMi8Warps)
       for (int i = 64 * lane; i < p.H; i += 64 * 32)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.X + (int64_t)t * p.H + i));
   }
@@ -360,11 +351,9 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   cluster_barrier();  // the masks are clear in the whole cluster
   if (!DOWN) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
-  mi8_route<PL, !DOWN>(p, r, s_scale, smem);  // (barriers within: the set-up above is visible after it)
+  mi8_route<PL, C, !DOWN>(p, r, s_scale, smem);  // (barriers within: the set-up above is visible after it)
   tc_fence_after();
   const uint32_t tmem = tmem_slot_mem;
-  if (!DOWN && blockIdx.x == 0)  // for kernel 2
-    for (int i = threadIdx.x; i < (p.H + kI8Rows - 1) / kI8Rows; i += blockDim.x) p.count[i] = 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // this CTA's units: (group, tile of weight rows)
@@ -577,37 +566,18 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
                  : "memory");
   }
   if constexpr (DOWN) {
-    // The last CTA of a column tile to arrive adds the splits' sums, in their order.
-    __shared__ int s_last;
-    if (col0 >= p.H) return;
-    const int tile = col0 / kI8Rows, n = p.M * kI8Rows;
-    if (p.split > 1) {
-      float* mine = p.part + ((int64_t)tile * p.split + first) * n;
-      for (int i = 4 * threadIdx.x; i < n; i += 4 * blockDim.x)
-        __stcg(reinterpret_cast<float4*>(mine + i), *reinterpret_cast<const float4*>(ysum + i));
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) s_last = atomicAdd(p.count + tile, 1) == p.split - 1;
-      __syncthreads();
-      if (!s_last) return;
-      __threadfence();
-    }
-    for (int i = 4 * threadIdx.x; i < n; i += 4 * blockDim.x) {
+    // The CTAs of a column tile lie in one cluster; each finishes a share of the tile's sums,
+    // adding its peers' in their order.
+    __syncwarp();
+    cluster_barrier();  // every CTA's sums are complete
+    const uint32_t peer0 = (uint32_t)(blockIdx.x % C - first);
+    for (int i = 4 * (first * (int)blockDim.x + (int)threadIdx.x); i < p.M * kI8Rows; i += 4 * p.split * (int)blockDim.x) {
       const int t = i / kI8Rows, c = col0 + i % kI8Rows;
       if (c >= p.H) continue;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p.split == 1) {
-        y = *reinterpret_cast<const float4*>(ysum + i);
-      } else {
-        // (16 in flight at once: four at a time the last CTA took 8 us for 32 tokens)
-        for (int q0 = 0; q0 < p.split; q0 += 16) {
-          float4 v[16];
-#pragma unroll
-          for (int q = 0; q < 16; ++q)
-            v[q] = mi8_ldcg_if(p.part + ((int64_t)tile * p.split + q0 + q) * n + i, q0 + q < p.split);
-#pragma unroll
-          for (int q = 0; q < 16; ++q) y.x += v[q].x, y.y += v[q].y, y.z += v[q].z, y.w += v[q].w;
-        }
+      for (int q = 0; q < p.split; ++q) {
+        const float4 v = ld_cluster_f4(ysum + i, peer0 + q);
+        y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
       }
       const int64_t at = (int64_t)t * p.H + c;  // (H % 16 == 0: four columns are in or out together)
       if (p.residual) {
@@ -616,6 +586,8 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
       }
       *reinterpret_cast<float4*>(p.Y + at) = y;
     }
+    __syncwarp();
+    cluster_barrier();  // no CTA leaves while its sums are read
   }
 }
 

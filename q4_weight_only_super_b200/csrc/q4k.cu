@@ -621,7 +621,7 @@ q4k_status launch_mi8_t(const CUtensorMap& tw, Mi8Params p, int grid, cudaStream
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kMi8Cluster;
+  attr[1].val.clusterDim.x = kMi8Cluster[DOWN];
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -629,10 +629,13 @@ q4k_status launch_mi8_t(const CUtensorMap& tw, Mi8Params p, int grid, cudaStream
   return launch_status(cudaLaunchKernelEx(&cfg, k, tw, p));
 }
 
-// CTAs per column tile of kernel 2: as many as keep one CTA per SM, at most one per expert.
+// CTAs per column tile of kernel 2: a power of two up to a cluster, about one CTA per SM, no
+// more than experts.
 int mi8_split(int M, int E, int topk, int H) {
-  const int tiles = (H + kI8Rows - 1) / kI8Rows;
-  return std::max(1, std::min({std::min(sm_count(), kMi8MaxCtas) / tiles, E, M * topk}));
+  const int tiles = (H + kI8Rows - 1) / kI8Rows, most = std::min(E, M * topk);
+  int s = kMi8Cluster[1];
+  while (s > 1 && (tiles * s > sm_count() * 9 / 8 || s / 2 >= most)) s /= 2;
+  return s;
 }
 
 template <int PL>
@@ -642,11 +645,11 @@ q4k_status launch_mi8(Mi8Params p, const int8_t* Wgu, const int8_t* Wd, cudaStre
     return Q4K_ERR_CUDA;
   // whole clusters; one CTA per SM, no more than units
   const int64_t most = (int64_t)p.M * p.topk * mi8_tiles(p.F);
-  auto whole = [](int64_t n) { return (int)((n + kMi8Cluster - 1) / kMi8Cluster * kMi8Cluster); };
-  const q4k_status st =
-      launch_mi8_t<PL, false>(tgu, p, whole(std::min<int64_t>(most, sm_count() / kMi8Cluster * kMi8Cluster)), s);
+  auto whole = [](int64_t n, int c) { return (int)((n + c - 1) / c * c); };
+  constexpr int c1 = kMi8Cluster[0], c2 = kMi8Cluster[1];
+  const q4k_status st = launch_mi8_t<PL, false>(tgu, p, whole(std::min<int64_t>(most, sm_count() / c1 * c1), c1), s);
   if (st != Q4K_OK) return st;
-  return launch_mi8_t<PL, true>(td, p, whole((int64_t)((p.H + kI8Rows - 1) / kI8Rows) * p.split), s);
+  return launch_mi8_t<PL, true>(td, p, whole((int64_t)((p.H + kI8Rows - 1) / kI8Rows) * p.split, c2), s);
 }
 
 }  // namespace
@@ -952,8 +955,6 @@ q4k_status moe_i8_layer(const float* logits, int M, int E, int topk, const int8_
   p.h = reinterpret_cast<float*>(w);
   w += mi8_ws_h(M, topk, F);
   p.hmax = reinterpret_cast<uint32_t*>(w);
-  p.count = reinterpret_cast<int32_t*>(w += mi8_ws_hmax(M, topk, F));
-  p.part = reinterpret_cast<float*>(w + ((H + kI8Rows - 1) / kI8Rows + 3) / 4 * 16);
   p.split = mi8_split(M, E, topk, H);
   p.M = M;
   p.E = E;
@@ -972,8 +973,8 @@ q4k_status moe_i8_layer(const float* logits, int M, int E, int topk, const int8_
 
 size_t q4k_workspace_bytes(int op, int M, int N, int K, int E, int topk) {
   if (op == Q4K_OP_MOE_I8) {
-    if (M <= 0 || N <= 0 || K <= 0 || topk <= 0) return 0;
-    return mi8_ws_bytes(M, topk, N, K);
+    if (M <= 0 || K <= 0 || topk <= 0) return 0;
+    return mi8_ws_bytes(M, topk, K);
   }
   if (op == Q4K_OP_ROUTE) {
     if (M <= 0 || E <= 0) return 0;
