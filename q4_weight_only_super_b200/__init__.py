@@ -358,7 +358,8 @@ def moe_combine_residual(O, inv_perm, topk_w, residual, M: int, topk: int, H: in
 
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
-_I8, _F32 = (torch.int8,), (torch.float32,)
+_int8, _float32, _bfloat16 = torch.int8, torch.float32, torch.bfloat16
+_I8, _F32 = (_int8,), (_float32,)
 
 
 def _need(fn, name, t, dtypes, shape, dev):
@@ -417,26 +418,35 @@ def i8_gemm(W, w_scale, X, x_scale, act: int = ACT_NONE, out_bf16: bool = False,
     """Y[m][n] = x_scale[m] * w_scale[n] * (X[m] . W[n]) from int8 W [N][K] and X [M][K];
     fp32, or bf16 with out_bf16 (or a bf16 Y). ACT_SWIGLU: bf16 [M][N/2], SiLU of the first
     N/2 channels times the others."""
-    fn, dev = "i8_gemm", W.get_device()
-    shape = N, K = _two_dims(fn, "W", W)
-    M = _two_dims(fn, "X", X)[0]
-    _need(fn, "W", W, _I8, shape, dev)
-    _need(fn, "w_scale", w_scale, _F32, (N,), dev)
-    _need(fn, "X", X, _I8, (M, K), dev)
-    _need(fn, "x_scale", x_scale, _F32, (M,), dev)
-    swiglu = act == ACT_SWIGLU
-    shape = (M, N // 2 if swiglu else N)
+    dev, swiglu = W.get_device(), act == ACT_SWIGLU
+    shape, x_shape = W.shape, X.shape
+    # one pass over what has to hold (a fifth of a small call's time); which of it does not is
+    # found out only then
+    if not (len(shape) == len(x_shape) == 2 and shape[1] == x_shape[1]
+            and W.dtype is X.dtype is _int8 and w_scale.dtype is x_scale.dtype is _float32
+            and w_scale.shape == shape[:1] and x_scale.shape == x_shape[:1]
+            and dev == X.get_device() == w_scale.get_device() == x_scale.get_device() >= 0
+            and W.is_contiguous() and X.is_contiguous() and w_scale.is_contiguous() and x_scale.is_contiguous()):
+        N, K = _two_dims("i8_gemm", "W", W)
+        M = _two_dims("i8_gemm", "X", X)[0]
+        _need("i8_gemm", "W", W, _I8, (N, K), dev)
+        _need("i8_gemm", "w_scale", w_scale, _F32, (N,), dev)
+        _need("i8_gemm", "X", X, _I8, (M, K), dev)
+        _need("i8_gemm", "x_scale", x_scale, _F32, (M,), dev)
+    N, K = shape
+    M = x_shape[0]
     if Y is None:
-        Y = _empty(shape, torch.bfloat16 if swiglu or out_bf16 else torch.float32, dev, stream)
+        Y = _empty((M, N // 2 if swiglu else N), _bfloat16 if swiglu or out_bf16 else _float32, dev, stream)
     else:
-        _need(fn, "Y", Y, (torch.bfloat16,) if swiglu or out_bf16 else (torch.float32, torch.bfloat16), shape, dev)
+        _need("i8_gemm", "Y", Y, (_bfloat16,) if swiglu or out_bf16 else (_float32, _bfloat16),
+              (M, N // 2 if swiglu else N), dev)
     if dev != _current_device():
         with torch.cuda.device(dev):
             return i8_gemm(W, w_scale, X, x_scale, act, out_bf16, Y, stream)
     st = lib().i8_gemm(W.data_ptr(), w_scale.data_ptr(), X.data_ptr(), x_scale.data_ptr(), Y.data_ptr(), M, N, K, act,
-                       Y.dtype == torch.bfloat16, _raw_stream(dev) if stream is None else _stream(stream))
+                       Y.dtype is _bfloat16, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
-        raise Q4KError(fn, st)
+        raise Q4KError("i8_gemm", st)
     return Y
 
 

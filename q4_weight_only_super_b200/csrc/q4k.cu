@@ -541,21 +541,44 @@ I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
   return best;
 }
 
-// i8_cut of the sizes that this thread asked for lately (a program has a few; the search
-// takes ~2 us of the host's time).
-const I8Cut& i8_cut_of(int M, int rows, int tile_rows, int K, int sms) {
-  struct Entry {
-    int M, rows, tile_rows, K, dev;
-    I8Cut cut;
-  };
+// What depends on the sizes alone of a product that this thread asked for lately (a program
+// has a few): its cut, which takes ~2 us of the host's time to find, and its tensor maps, in
+// which a call puts its own addresses.
+struct I8Plan {
+  int M, N, K, swiglu, dev;
+  I8Cut cut;
+  int boxed;
+  CUtensorMap tw, tx;
+};
+
+I8Plan* i8_plan(int M, int N, int K, bool swiglu, const void* W, const void* X, int sms) {
   constexpr unsigned kEntries = 64;
-  static thread_local Entry table[kEntries];
+  static thread_local I8Plan table[kEntries];
+  static PFN_cuTensorMapReplaceAddress_v12000 replace = nullptr;
+  if (!replace) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPoint("cuTensorMapReplaceAddress", &ptr, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return nullptr;
+    replace = reinterpret_cast<PFN_cuTensorMapReplaceAddress_v12000>(ptr);
+  }
   const int dev = current_device();
-  const unsigned h = ((unsigned)M * 2654435761u ^ (unsigned)rows * 40503u ^ (unsigned)K * 2246822519u) >> 7;
-  Entry& e = table[h % kEntries];
-  if (e.M != M || e.rows != rows || e.tile_rows != tile_rows || e.K != K || e.dev != dev)
-    e = {M, rows, tile_rows, K, dev, i8_cut(M, rows, tile_rows, K, sms)};
-  return e.cut;
+  const unsigned h = ((unsigned)M * 2654435761u ^ (unsigned)N * 40503u ^ (unsigned)K * 2246822519u) >> 7;
+  I8Plan& e = table[(h + swiglu) % kEntries];
+  if (e.M == M && e.N == N && e.K == K && e.swiglu == (int)swiglu && e.dev == dev)
+    return replace(&e.tw, const_cast<void*>(W)) == CUDA_SUCCESS && replace(&e.tx, const_cast<void*>(X)) == CUDA_SUCCESS
+               ? &e
+               : nullptr;
+  const int rows = swiglu ? N / 2 : N;
+  e.M = 0;  // (not a plan, until it is whole)
+  e.cut = i8_cut(M, rows, swiglu ? kI8Rows / 2 : kI8Rows, K, sms);
+  e.boxed = swiglu && rows % 16 == 0;
+  if (!(e.boxed ? make_tmap_gate_up(&e.tw, W, 1, rows, K) : make_tmap_i8(&e.tw, W, N, K, swiglu ? 16 : kI8Rows)) ||
+      !make_tmap_i8(&e.tx, X, M, K, e.cut.nt / (1 + e.cut.pair)))
+    return nullptr;
+  e.M = M, e.N = N, e.K = K, e.swiglu = swiglu, e.dev = dev;
+  return &e;
 }
 
 template <bool SWIGLU, bool BF16, bool PAIR>
@@ -578,23 +601,21 @@ q4k_status i8_gemm_t(const int8_t* W, const int8_t* X, I8GemmParams p, cudaStrea
   if (sms <= 0) return Q4K_ERR_CUDA;
   const int rows = SWIGLU ? p.N / 2 : p.N, tile_rows = SWIGLU ? kI8Rows / 2 : kI8Rows;
   if (((int64_t)rows / tile_rows + 2) * (p.M / kI8MaxNT + 4) > 0x7fffffffLL / 16) return Q4K_ERR_UNSUPPORTED;
-  const I8Cut& c = i8_cut_of(p.M, rows, tile_rows, p.K, sms);
+  const I8Plan* plan = i8_plan(p.M, p.N, p.K, SWIGLU, W, X, sms);
+  if (!plan) return Q4K_ERR_CUDA;
+  const I8Cut& c = plan->cut;
   p.nt = c.nt;
   p.n_tiles = c.n_tiles;
   p.m_tiles = c.m_tiles;
   p.stages = c.stages;
   p.ksplit = c.ksplit;
+  p.boxed = plan->boxed;
   p.tail = c.stages * (int)(kI8ATile + (size_t)(c.nt / (1 + c.pair)) * kI8KB);
   p.tstride = (p.nt + 31) / 32 * 32;
   p.tmem_cols = 32;
   while (p.tmem_cols < (c.ksplit > 1 ? 1 : 2) * p.tstride) p.tmem_cols *= 2;
-  CUtensorMap tw, tx;
-  p.boxed = SWIGLU && rows % 16 == 0;
-  if (!(p.boxed ? make_tmap_gate_up(&tw, W, 1, rows, p.K) : make_tmap_i8(&tw, W, p.N, p.K, SWIGLU ? 16 : kI8Rows)) ||
-      !make_tmap_i8(&tx, X, p.M, p.K, p.nt / (1 + c.pair)))
-    return Q4K_ERR_CUDA;
-  return c.pair ? i8_gemm_cut<SWIGLU, BF16, true>(c, tw, tx, p, sms, s)
-                : i8_gemm_cut<SWIGLU, BF16, false>(c, tw, tx, p, sms, s);
+  return c.pair ? i8_gemm_cut<SWIGLU, BF16, true>(c, plan->tw, plan->tx, p, sms, s)
+                : i8_gemm_cut<SWIGLU, BF16, false>(c, plan->tw, plan->tx, p, sms, s);
 }
 
 // Shared memory of the layer's kernels: half of an SM's, so that a CTA of kernel 2 finds
