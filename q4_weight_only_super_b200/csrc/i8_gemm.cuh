@@ -210,7 +210,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
   auto bar_tempty = [&](int a) { return bars + 8u * (2 * kI8MaxStages + 2 + a); };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + p.tail + 8 * (2 * kI8MaxStages + 4));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + p.tail + 8 * (2 * kI8MaxStages + 4) + 4);
-  float* s_xs = reinterpret_cast<float*>(smem + p.tail + 256);  // [epilogue warps][kI8MaxNT] token scales
+  float* s_xs = reinterpret_cast<float*>(smem + p.tail + 256);  // [epilogue warps][nt] token scales
 
   // place in the cluster: ranks P s + r: half r of the pair, share s of K
   const int csize = SPLIT ? P * p.ksplit : P;
@@ -359,7 +359,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
     int done = 0;
     const int64_t ldy = SWIGLU ? half : p.N;
     const int rows = SWIGLU ? half : p.N;
-    float* xs = s_xs + (warp - 2) * kI8MaxNT;  // a copy per warp: no barrier between warps, which may stop apart
+    float* xs = s_xs + (warp - 2) * p.nt;  // a copy per warp: no barrier between warps, which may stop apart
     for (int tile = first; tile < tiles; tile += step, ++done) {
       const int a = done & 1;
       const int m0 = tile_m0(tile);

@@ -434,7 +434,7 @@ q4k_status noalloc_route_scratch(int32_t** out) {
 // Shared memory of one product CTA: the whole SM's, or half of it (two CTAs per SM) for
 // lone CTAs on narrow token tiles, whose accumulators then fit half the TMEM too.
 constexpr size_t kI8Smem[2] = {232448, kGemvTwoPerSm};
-constexpr size_t kI8TailBytes = 256 + kI8EpiWarps * kI8MaxNT * sizeof(float);
+constexpr size_t i8_tail_bytes(int nt) { return 256 + kI8EpiWarps * nt * sizeof(float); }  // barriers, scales
 
 template <typename F>
 q4k_status i8_launch(F* k, const CUtensorMap& tw, const CUtensorMap& tx, const I8GemmParams& p, int grid, int cluster,
@@ -513,7 +513,7 @@ I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
       if (c.nt > kI8MaxNT) continue;
       c.n_tiles = (rows + tile_rows * P - 1) / (tile_rows * P);
       const size_t stage = kI8ATile + (size_t)(c.nt / P) * kI8KB;
-      c.stages = std::min<int>(kI8MaxStages, (int)((kI8Smem[c.halved] - 1024 - kI8TailBytes) / stage));
+      c.stages = std::min<int>(kI8MaxStages, (int)((kI8Smem[c.halved] - 1024 - i8_tail_bytes(c.nt)) / stage));
       const double tiles = (double)c.n_tiles * mt;
       const double work = std::max(1.18 * c.nt, stage / 111.), ring = 1120. / std::min(c.stages, 3);
       for (int ks = 1; ks <= std::min(8 / P, nk); ++ks) {
