@@ -51,12 +51,6 @@ __device__ __forceinline__ uint4 ldg_u4(const void* p) {
   return v;
 }
 
-__device__ __forceinline__ uint4 lds_u4(uint32_t saddr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr));
-  return v;
-}
-
 // ---- Q4_K field decode ----------------------------------------------------
 
 __device__ __forceinline__ float half_bits_to_float(uint32_t h16) {

@@ -117,7 +117,8 @@ __device__ __forceinline__ void mi8_topk(const uint32_t (&key)[PL], int topk, in
   for (int c = lane; c < count; c += 32) {
     const uint64_t mine = list[c];
     int before = 0;
-    for (int j = 0; j < count; ++j) before += list[j] > mine;
+    // (the list is in the order of the ids: among many equal logits topk steps decide)
+    for (int j = 0; j < count && before < topk; ++j) before += list[j] > mine;
     if (before < topk) {
       id[before] = (uint16_t)(0xffffffffu - (uint32_t)mine);
       keys[before] = (uint32_t)(mine >> 32);
@@ -191,7 +192,7 @@ __device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r, f
   for (int t = rank + C * warp; t < p.M; t += C * kMi8Warps) {
     uint32_t key[PL];
 #pragma unroll
-    for (int j = 0; j < PL; ++j) key[j] = 32 * j + lane < p.E ? mi8_key(p.logits[(int64_t)t * p.E + 32 * j + lane]) : 0u;
+    for (int j = 0; j < PL; ++j) key[j] = 32 * j + lane < p.E ? mi8_key(__ldcg(p.logits + (int64_t)t * p.E + 32 * j + lane)) : 0u;
     uint16_t* id = r.id + t * p.topk;
     uint32_t* w = r.w + t * p.topk;
     mi8_topk<PL>(key, p.topk, lane, list, id, w);

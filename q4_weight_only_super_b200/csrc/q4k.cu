@@ -554,15 +554,15 @@ struct I8Plan {
 I8Plan* i8_plan(int M, int N, int K, bool swiglu, const void* W, const void* X, int sms) {
   constexpr unsigned kEntries = 64;
   static thread_local I8Plan table[kEntries];
-  static PFN_cuTensorMapReplaceAddress_v12000 replace = nullptr;
-  if (!replace) {
+  static const auto replace = []() -> PFN_cuTensorMapReplaceAddress_v12000 {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPoint("cuTensorMapReplaceAddress", &ptr, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      return nullptr;
-    replace = reinterpret_cast<PFN_cuTensorMapReplaceAddress_v12000>(ptr);
-  }
+    const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapReplaceAddress", &ptr, cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<PFN_cuTensorMapReplaceAddress_v12000>(ptr)
+               : nullptr;
+  }();
+  if (!replace) return nullptr;
   const int dev = current_device();
   const unsigned h = ((unsigned)M * 2654435761u ^ (unsigned)N * 40503u ^ (unsigned)K * 2246822519u) >> 7;
   I8Plan& e = table[(h + swiglu) % kEntries];

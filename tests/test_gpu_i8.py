@@ -299,6 +299,25 @@ def test_moe_equal_logits_go_to_the_lower_id():
     check_moe(q.moe_i8_layer(L, 4, Wg, sg, Wd, sd, X), L, 4, Wg, sg, Wd, sd, X)
 
 
+def test_moe_equal_logits_of_many_experts():
+    L, Wg, sg, Wd, sd, X = moe_inputs(27, 32, 1000, 32, 16)
+    L[:30] = 0.25
+    L[1, 960:] = 0.5  # the larger ones behind
+    L[2] = torch.arange(1000, device="cuda") // 100  # ties at the last selected one
+    check_moe(q.moe_i8_layer(L, 16, Wg, sg, Wd, sd, X), L, 16, Wg, sg, Wd, sd, X)
+
+
+def test_moe_token_with_every_expert_masked_stays_alone():
+    L, Wg, sg, Wd, sd, X = moe_inputs(28, 5, 12, 64, 48)
+    L[2] = -float("inf")
+    L[3, 1:] = -float("inf")  # one expert left: the others weigh nothing
+    L[4] = torch.finfo(torch.float32).min  # the lowest value is a value: equal weights
+    Y = q.moe_i8_layer(L, 4, Wg, sg, Wd, sd, X)
+    assert torch.isnan(Y[2]).all()
+    rest = [0, 1, 3, 4]
+    check_moe(Y[rest], L[rest], 4, Wg, sg, Wd, sd, X[rest])
+
+
 def test_moe_nan_logits_rank_last():
     L, Wg, sg, Wd, sd, X = moe_inputs(22, 3, 12, 64, 48)
     L[1, [0, 4, 7]] = float("nan")
