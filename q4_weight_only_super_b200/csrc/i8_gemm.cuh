@@ -151,8 +151,8 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
 }
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, int32_t a, int32_t b, int32_t c, int32_t d) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+__device__ __forceinline__ void st_cluster_s32(uint32_t addr, int32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // A place in a ring of stages, and the parity of its pass (the roles' single threads pay
@@ -187,10 +187,6 @@ __device__ __forceinline__ int i8_row(int n_tile, int q, int lane, bool* up) {
   *up = lane >= 16;
   return n_tile * (kI8Rows / 2) + 16 * q + (lane & 15);
 }
-
-// Words between the rows of a SPLIT share of `per` (a multiple of 4) token columns: an odd
-// number of 16-byte pieces, so that eight rows' pieces lie in different banks.
-__host__ __device__ __forceinline__ int i8_part_pitch(int per) { return per / 4 % 2 ? per : per + 4; }
 
 template <bool SWIGLU, bool BF16, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(kI8Threads, 2)
@@ -413,8 +409,10 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
     const int m0 = tile_m0(first), nti = tile_n(first);
     const int mcount = min(p.nt, p.M - m0);
     const int per = ((p.nt + p.ksplit - 1) / p.ksplit + 3) / 4 * 4;  // token columns that a CTA sums and stores
-    const int pitch = i8_part_pitch(per);
-    int32_t* part = reinterpret_cast<int32_t*>(smem);  // [ksplit][128][pitch]: the stages are free by then
+    // [ksplit][per][128]: the stages are free by then. A warp sends 32 neighbouring rows of a
+    // column, 128 bytes in a row: peers' shared memory takes about a request every 3 cycles
+    // whatever its size (16 bytes of a row at a time: 300 x 5120 x 17408 spent 10 us here)
+    int32_t* part = reinterpret_cast<int32_t*>(smem);
     const int q = warp & 3, turn = (warp - 2) >> 2;
     bool ok = true;
     if (warp >= 2) {
@@ -426,15 +424,18 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
     if (warp >= 2 && ok) {
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16);
-      const uint32_t mine = sbase + (uint32_t)((ks * kI8Rows + 32 * q + lane) * pitch) * 4u;
+      const uint32_t mine = sbase + (uint32_t)(ks * per * kI8Rows + 32 * q + lane) * 4u;
       int to = 16 * turn / per, left = 16 * turn % per;  // whose column comes next, and where in the share
       for (int c = 16 * turn; c < mcount; c += 16 * (kI8EpiWarps / 4)) {
         int32_t v[16];
         tmem_ld16(d + c, v);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          if (c + i < mcount)
-            st_cluster_v4(cluster_addr(mine + 4u * left, (uint32_t)(P * to + r)), v[i], v[i + 1], v[i + 2], v[i + 3]);
+          if (c + i < mcount) {
+            const uint32_t at = cluster_addr(mine + (uint32_t)(left * kI8Rows) * 4u, (uint32_t)(P * to + r));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) st_cluster_s32(at + (uint32_t)(j * kI8Rows) * 4u, v[i + j]);
+          }
           if ((left += 4) >= per) left -= per, ++to;
         }
         for (left += 16 * (kI8EpiWarps / 4 - 1); left >= per; left -= per) ++to;
@@ -449,8 +450,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
       auto sum = [&](int c, int row, float (&y)[4]) {
         int32_t t[4] = {0, 0, 0, 0};
         for (int s = 0; s < p.ksplit; ++s) {
-          const int4 v = *reinterpret_cast<const int4*>(part + (s * kI8Rows + row) * pitch + c);
-          t[0] += v.x, t[1] += v.y, t[2] += v.z, t[3] += v.w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] += part[(s * per + c + i) * kI8Rows + row];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = (float)t[i] * s_xs[min(c0 + c + i, mcount - 1)];

@@ -524,7 +524,7 @@ I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
         if (ks > 1) {
           const int per = ((c.nt + ks - 1) / ks + 3) / 4 * 4;
           if (tiles > (double)i8_cluster_fit(P * ks) * (1 + c.halved)) continue;
-          if ((size_t)ks * kI8Rows * i8_part_pitch(per) * 4 > c.stages * stage) continue;
+          if ((size_t)ks * kI8Rows * per * 4 > c.stages * stage) continue;
         }
         const double waves = std::ceil(ctas / (sms * (1 + c.halved)));
         const double share = c.halved && ctas > sms ? 2 : 1;
