@@ -124,11 +124,14 @@ __device__ __forceinline__ void tma2_load_gate_up(uint32_t dst, const CUtensorMa
       : "memory");
 }
 
-// silu(g) * u as silu_mul, the quotient by a reciprocal: 1 + e lies in [1, 2], where
-// __fdividef is within 2 ulp.
+// silu(g) * u = g u a^2 / (1 + h^2), h = exp(-|g| / 2), a = 1 or, g < 0, h: for a result that is
+// rounded to bf16. The exponential by ex2 is off by 2 + 0.6 |g| ulp (2^-23), the quotient (1 +
+// h^2 lies in [1, 2]) by 2: together below 2^-16 of the result for |g| < 90. By halves, exp(-|g|)
+// does not leave fp32's range before silu(g) does. (With expf, tokens and 64-bit offsets one by
+// one, the epilogue of 128 x 256 sums took 12 us, longer than the MMAs of 5120 in K.)
 __device__ __forceinline__ float i8_silu_mul(float g, float u) {
-  const float e = expf(-fabsf(g));
-  return g * __fdividef(g >= 0.f ? 1.f : e, 1.f + e) * u;
+  const float h = __expf(-0.5f * fabsf(g)), a = g >= 0.f ? 1.f : h;
+  return g * __fdividef(a, fmaf(h, h, 1.f)) * (a * u);
 }
 
 // Instruction descriptor of kind::i8: int32 accumulators (2), signed A and B (1), both
@@ -372,13 +375,25 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
         int32_t v[16];
         tmem_ld16(d + c, v);
         if (SWIGLU) {
+          // lanes of the gate finish the even tokens, those of up the odd ones
+          const int64_t at = (int64_t)(m0 + c + (up ? 1 : 0)) * ldy + n;
+          float hv[8];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float y0 = (float)v[i] * xs[c + i] * w, y1 = (float)v[i + 1] * xs[c + i + 1] * w;
-            const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
-            const float hv = up ? i8_silu_mul(got, y1) : i8_silu_mul(y0, got);
-            const int m = c + i + (up ? 1 : 0);
-            if (m < mcount && n < rows) i8_store<BF16>(p.Y, (int64_t)(m0 + m) * ldy + n, hv);
+          for (int i = 0; i < 16; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(xs + c + i);
+            const float y[4] = {(float)v[i] * x.x * w, (float)v[i + 1] * x.y * w, (float)v[i + 2] * x.z * w,
+                                (float)v[i + 3] * x.w * w};
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              const float got = __shfl_xor_sync(0xffffffffu, up ? y[j] : y[j + 1], 16), kept = up ? y[j + 1] : y[j];
+              hv[(i + j) / 2] = i8_silu_mul(up ? got : kept, up ? kept : got);
+            }
+          }
+          if (n < rows) {
+            const int left = mcount - c - (up ? 1 : 0);  // tokens from this lane's first on
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (2 * i < left) i8_store<BF16>(p.Y, at + 2 * i * ldy, hv[i]);
           }
         } else if (n < rows) {
           const int64_t at = (int64_t)(m0 + c) * ldy + n;
