@@ -125,13 +125,16 @@ __device__ __forceinline__ void tma2_load_gate_up(uint32_t dst, const CUtensorMa
 }
 
 // silu(g) * u = g u a^2 / (1 + h^2), h = exp(-|g| / 2), a = 1 or, g < 0, h: for a result that is
-// rounded to bf16. The exponential by ex2 is off by 2 + 0.6 |g| ulp (2^-23), the quotient (1 +
-// h^2 lies in [1, 2]) by 2: together below 2^-16 of the result for |g| < 90. By halves, exp(-|g|)
+// rounded to bf16. The exponential by ex2 is off by 2 + 0.6 |g| ulp (2^-23), the reciprocal (of
+// 1 to 2) by 1: together below 2^-16 of the result for |g| < 90. By halves, exp(-|g|)
 // does not leave fp32's range before silu(g) does. (With expf, tokens and 64-bit offsets one by
 // one, the epilogue of 128 x 256 sums took 12 us, longer than the MMAs of 5120 in K.)
 __device__ __forceinline__ float i8_silu_mul(float g, float u) {
-  const float h = __expf(-0.5f * fabsf(g)), a = g >= 0.f ? 1.f : h;
-  return g * __fdividef(a, fmaf(h, h, 1.f)) * (a * u);
+  float h, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(fabsf(g) * -0.72134752f));  // -log2(e) / 2
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(h, h, 1.f)));
+  const float a = g >= 0.f ? 1.f : h;
+  return g * (a * r) * (a * u);
 }
 
 // Instruction descriptor of kind::i8: int32 accumulators (2), signed A and B (1), both
@@ -430,6 +433,11 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
     int32_t* part = reinterpret_cast<int32_t*>(smem);
     const int q = warp & 3, turn = (warp - 2) >> 2;
     bool ok = true;
+    // the row that this thread sums, and its scales, asked for early
+    constexpr int kCols = SWIGLU ? 64 : 128, kStep = 32 * kI8EpiWarps / kCols * 4;
+    const int et = threadIdx.x - 64, n = nti * kCols + et % kCols;
+    const bool in = et >= 0 && n < (SWIGLU ? half : p.N);
+    const float w = in ? p.ws[n] : 0.f, wu = SWIGLU && in ? p.ws[half + n] : 0.f;
     if (warp >= 2) {
       for (int i = threadIdx.x - 64; i < mcount; i += 32 * kI8EpiWarps) s_xs[i] = p.xs[m0 + i];
       ok = __all_sync(0xffffffffu, mbar_wait_l(bar_tfull(0), 0, abort_flag, limit));
@@ -460,31 +468,29 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
     __syncwarp();
     cluster_barrier();
     if (warp >= 2 && ok) {
-      const int et = threadIdx.x - 64;
       const int c0 = ks * per, c1 = min(per, mcount - c0);  // this CTA's columns of the tile
       auto sum = [&](int c, int row, float (&y)[4]) {
         int32_t t[4] = {0, 0, 0, 0};
-        for (int s = 0; s < p.ksplit; ++s) {
+        const int32_t* from = part + c * kI8Rows + row;
+#pragma unroll 4
+        for (int s = 0; s < p.ksplit; ++s, from += per * kI8Rows) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) t[i] += part[(s * per + c + i) * kI8Rows + row];
+          for (int i = 0; i < 4; ++i) t[i] += from[i * kI8Rows];
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = (float)t[i] * s_xs[min(c0 + c + i, mcount - 1)];
+        const float4 x = *reinterpret_cast<const float4*>(s_xs + c0 + c);  // (past mcount: no one's)
+        y[0] = (float)t[0] * x.x, y[1] = (float)t[1] * x.y, y[2] = (float)t[2] * x.z, y[3] = (float)t[3] * x.w;
       };
-      constexpr int kCols = SWIGLU ? 64 : 128, kStep = 32 * kI8EpiWarps / kCols * 4;
-      const int n = nti * kCols + et % kCols;
       const int64_t ldy = SWIGLU ? half : p.N;
-      if (n < (SWIGLU ? half : p.N)) {
-        const float w = p.ws[n], wu = SWIGLU ? p.ws[half + n] : 0.f;
+      if (in) {
         const int row = SWIGLU ? 32 * (et % 64 / 16) + et % 16 : et % 128;
         for (int c = et / kCols * 4; c < c1; c += kStep) {
           float y[4], u[4];
           sum(c, row, y);
           if (SWIGLU) sum(c, row + 16, u);
+          const int64_t at = (int64_t)(m0 + c0 + c) * ldy + n;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (c + i < c1)
-              i8_store<BF16>(p.Y, (int64_t)(m0 + c0 + c + i) * ldy + n, SWIGLU ? i8_silu_mul(y[i] * w, u[i] * wu) : y[i] * w);
+            if (c + i < c1) i8_store<BF16>(p.Y, at + i * ldy, SWIGLU ? i8_silu_mul(y[i] * w, u[i] * wu) : y[i] * w);
         }
       }
     }
