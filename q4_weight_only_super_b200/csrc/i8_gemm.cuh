@@ -129,12 +129,20 @@ __device__ __forceinline__ void tma2_load_gate_up(uint32_t dst, const CUtensorMa
 // 1 to 2) by 1: together below 2^-16 of the result for |g| < 90. By halves, exp(-|g|)
 // does not leave fp32's range before silu(g) does. (With expf, tokens and 64-bit offsets one by
 // one, the epilogue of 128 x 256 sums took 12 us, longer than the MMAs of 5120 in K.)
-__device__ __forceinline__ float i8_silu_mul(float g, float u) {
-  float h, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(fabsf(g) * -0.72134752f));  // -log2(e) / 2
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(h, h, 1.f)));
-  const float a = g >= 0.f ? 1.f : h;
-  return g * (a * r) * (a * u);
+// V of them at once, step by step: their latencies overlap.
+template <int V>
+__device__ __forceinline__ void i8_silu_mul(const float (&g)[V], const float (&u)[V], float (&out)[V]) {
+  float h[V], r[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(h[i]) : "f"(fabsf(g[i]) * -0.72134752f));  // -log2(e) / 2
+#pragma unroll
+  for (int i = 0; i < V; ++i) asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[i]) : "f"(fmaf(h[i], h[i], 1.f)));
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float a = g[i] >= 0.f ? 1.f : h[i];
+    out[i] = g[i] * (a * r[i]) * (a * u[i]);
+  }
 }
 
 // Instruction descriptor of kind::i8: int32 accumulators (2), signed A and B (1), both
@@ -175,11 +183,11 @@ struct I8Ring {
 };
 
 template <bool BF16>
-__device__ __forceinline__ void i8_store(void* Y, int64_t at, float v) {
+__device__ __forceinline__ void i8_store(uint8_t* at, float v) {
   if (BF16)
-    static_cast<__nv_bfloat16*>(Y)[at] = __float2bfloat16_rn(v);
+    *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(v);
   else
-    static_cast<float*>(Y)[at] = v;
+    *reinterpret_cast<float*>(at) = v;
 }
 
 // The output channel (row of W) that lane `lane` of TMEM quadrant q holds in a tile: its
@@ -359,8 +367,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
     // ---------------- epilogue ----------------
     const int q = warp & 3, turn = (warp - 2) >> 2;
     int done = 0;
-    const int64_t ldy = SWIGLU ? half : p.N;
     const int rows = SWIGLU ? half : p.N;
+    constexpr int kOut = BF16 ? 2 : 4;
+    const int64_t pitch = (int64_t)rows * kOut;
     float* xs = s_xs + (warp - 2) * p.nt;  // a copy per warp: no barrier between warps, which may stop apart
     for (int tile = first; tile < tiles; tile += step, ++done) {
       const int a = done & 1;
@@ -370,6 +379,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
       bool up;
       const int n = i8_row<SWIGLU>(tile_n(tile), q, lane, &up);
       const float w = n < rows ? p.ws[up ? half + n : n] : 0.f;
+      uint8_t* col = static_cast<uint8_t*>(p.Y) + (int64_t)n * kOut;  // the channel's outputs, a pitch apart
       __syncwarp();
       if (!__all_sync(0xffffffffu, mbar_wait_l(bar_tfull(a), (done / 2) & 1, abort_flag, limit))) break;
       tc_fence_after();
@@ -379,8 +389,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
         tmem_ld16(d + c, v);
         if (SWIGLU) {
           // lanes of the gate finish the even tokens, those of up the odd ones
-          const int64_t at = (int64_t)(m0 + c + (up ? 1 : 0)) * ldy + n;
-          float hv[8];
+          float g[8], u[8];
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             const float4 x = *reinterpret_cast<const float4*>(xs + c + i);
@@ -388,25 +397,36 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
                                 (float)v[i + 3] * x.w * w};
 #pragma unroll
             for (int j = 0; j < 4; j += 2) {
-              const float got = __shfl_xor_sync(0xffffffffu, up ? y[j] : y[j + 1], 16), kept = up ? y[j + 1] : y[j];
-              hv[(i + j) / 2] = i8_silu_mul(up ? got : kept, up ? kept : got);
+              const float got = __shfl_xor_sync(0xffffffffu, up ? y[j] : y[j + 1], 16);
+              g[(i + j) / 2] = up ? got : y[j];
+              u[(i + j) / 2] = up ? y[j + 1] : got;
             }
           }
+          float hv[8];
+          i8_silu_mul(g, u, hv);
           if (n < rows) {
             const int left = mcount - c - (up ? 1 : 0);  // tokens from this lane's first on
+            uint8_t* at = col + (m0 + c + (up ? 1 : 0)) * pitch;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (2 * i < left) i8_store<BF16>(p.Y, at + 2 * i * ldy, hv[i]);
+            for (int i = 0; i < 8; ++i, at += 2 * pitch)
+              if (2 * i < left) i8_store<BF16>(at, hv[i]);
           }
         } else if (n < rows) {
-          const int64_t at = (int64_t)(m0 + c) * ldy + n;
+          uint8_t* at = col + (m0 + c) * pitch;
+          float y[16];
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(xs + c + i);
+            y[i] = (float)v[i] * x.x * w, y[i + 1] = (float)v[i + 1] * x.y * w;
+            y[i + 2] = (float)v[i + 2] * x.z * w, y[i + 3] = (float)v[i + 3] * x.w * w;
+          }
           if (c + 16 <= mcount) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) i8_store<BF16>(p.Y, at + i * ldy, (float)v[i] * xs[c + i] * w);
+            for (int i = 0; i < 16; ++i, at += pitch) i8_store<BF16>(at, y[i]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c + i < mcount) i8_store<BF16>(p.Y, at + i * ldy, (float)v[i] * xs[c + i] * w);
+            for (int i = 0; i < 16; ++i, at += pitch)
+              if (c + i < mcount) i8_store<BF16>(at, y[i]);
           }
         }
         __syncwarp();
@@ -480,17 +500,23 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
         const float4 x = *reinterpret_cast<const float4*>(s_xs + c0 + c);  // (past mcount: no one's)
         y[0] = (float)t[0] * x.x, y[1] = (float)t[1] * x.y, y[2] = (float)t[2] * x.z, y[3] = (float)t[3] * x.w;
       };
-      const int64_t ldy = SWIGLU ? half : p.N;
       if (in) {
+        constexpr int kOut = BF16 ? 2 : 4;
+        const int64_t pitch = (int64_t)(SWIGLU ? half : p.N) * kOut;
+        const int first_c = et / kCols * 4;
+        uint8_t* at = static_cast<uint8_t*>(p.Y) + (m0 + c0 + first_c) * pitch + (int64_t)n * kOut;
         const int row = SWIGLU ? 32 * (et % 64 / 16) + et % 16 : et % 128;
-        for (int c = et / kCols * 4; c < c1; c += kStep) {
-          float y[4], u[4];
+        for (int c = first_c; c < c1; c += kStep, at += kStep * pitch) {
+          float y[4], u[4] = {};
           sum(c, row, y);
           if (SWIGLU) sum(c, row + 16, u);
-          const int64_t at = (int64_t)(m0 + c0 + c) * ldy + n;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] *= w, u[i] *= wu;
+          float out[4];
+          if (SWIGLU) i8_silu_mul(y, u, out);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (c + i < c1) i8_store<BF16>(p.Y, at + i * ldy, SWIGLU ? i8_silu_mul(y[i] * w, u[i] * wu) : y[i] * w);
+            if (c + i < c1) i8_store<BF16>(at + i * pitch, SWIGLU ? out[i] : y[i]);
         }
       }
     }
