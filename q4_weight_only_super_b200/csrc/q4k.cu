@@ -489,16 +489,17 @@ struct I8Cut {
 };
 
 // The cut with the least estimated time, in SM cycles. A stage (128 bytes of K of a CTA's
-// tiles) takes 1.18 cycles a token for the MMAs, or its bytes at 111 a cycle from L2, and
-// not less than the ring's latency allows; weights and tokens come from DRAM at 2380 bytes a
-// cycle; the smaller of the two is not hidden by the larger altogether; a K split pays for
-// its exchange, a pair for its hand-shakes. The constants are fitted to 29 shapes (1 .. 3000
-// tokens, 200 .. 34816 channels, K 512 .. 17408), every cut of each measured, and mean nothing
-// beyond that: the chosen cut is 1.5% slower than the fastest in the mean, 12% at most (1500 x
-// 600 x 4096: 15.5 for 13.8 us; 37 x 2051 x 2064: 6.8 for 6.1 us).
+// tiles) takes 1.63 cycles a token for the MMAs, or its bytes at 94 a cycle from L2, and
+// not less than the ring's latency allows; more where SMs may get two CTAs. Weights and tokens
+// come from DRAM at 3310 bytes a cycle, and the smaller of the two is not hidden by the larger
+// altogether. Then the epilogue, of a K split with its exchange, and a pair's hand-shakes. The
+// constants are fitted to 38 shapes (1 .. 3000 tokens, 200 .. 34816 channels, K 512 .. 17408),
+// every cut of each measured, and mean nothing beyond that: the chosen cut is 1.5% slower than
+// the fastest in the mean, 10% at most (250 x 30000 x 512: 13.3 for 12.0 us; 37 x 2051 x 2064:
+// 5.7 for 5.4).
 I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
   const int nk = (K + kI8KB - 1) / kI8KB;
-  const double dram = ((double)rows * (kI8Rows / tile_rows) + M) * K / 2380.;
+  const double dram = ((double)rows * (kI8Rows / tile_rows) + M) * K / 3310.;
   I8Cut best = {};
   double least = 1e300;
   for (int form = 0; form < 4; ++form) {  // lone CTAs or pairs, one CTA per SM or two
@@ -515,7 +516,7 @@ I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
       const size_t stage = kI8ATile + (size_t)(c.nt / P) * kI8KB;
       c.stages = std::min<int>(kI8MaxStages, (int)((kI8Smem[c.halved] - 1024 - i8_tail_bytes(c.nt)) / stage));
       const double tiles = (double)c.n_tiles * mt;
-      const double work = std::max(1.18 * c.nt, stage / 111.), ring = 1120. / std::min(c.stages, 3);
+      const double work = std::max(1.63 * c.nt, stage / 94.), ring = 920. / std::min(c.stages, 3);
       for (int ks = 1; ks <= std::min(8 / P, nk); ++ks) {
         // two CTAs share an SM's 512 TMEM columns, and a CTA that walks tiles has two accumulators
         if (c.halved && (ks > 1 ? 1 : 2) * c.nt > 256) continue;
@@ -527,10 +528,10 @@ I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
           if ((size_t)ks * kI8Rows * per * 4 > c.stages * stage) continue;
         }
         const double waves = std::ceil(ctas / (sms * (1 + c.halved)));
-        const double share = c.halved && ctas > sms ? 2 : 1;
+        const double share = !c.halved ? 1 : ctas > sms ? 2 : 1.48;
         const double mma = waves * std::ceil((double)nk / ks) * std::max(share * work, ring);
-        const double t = std::max(mma, dram) + 0.172 * std::min(mma, dram) +
-                         (ks > 1 ? 2615. + 5.6 * c.nt + 369. * ks : 2.6 * c.nt) + 367. * pair;
+        const double t = std::max(mma, dram) + 0.52 * std::min(mma, dram) +
+                         (ks > 1 ? 27.8 * c.nt + 365. * ks : 17.5 * c.nt) + 1470. * pair;
         if (t < least) {
           least = t;
           best = c;
