@@ -15,9 +15,9 @@
 // That keeps what fp32 sums would (X: S is a power of two, so a bf16 value within 2^14 of
 // its row's largest is exact; h: to 2^-23 of its row's largest), costs no instruction per
 // weight, and makes the sums independent of their order.
-// Measured (128 experts, top-8, H = 2048, F = 768): 20.2 / 58.5 / 114 us for 1 / 8 / 32 tokens,
-// 1.9 / 4.2 / 4.6 TB/s of the weights that have to be read; the streams themselves run at 5.4 to
-// 6 TB/s, the rest is routing, the hand-over between the kernels and the last sums. mma.sync
+// Measured (128 experts, top-8, H = 2048, F = 768): 19.7 / 58.8 / 115 us for 1 / 8 / 32 tokens,
+// 1.9 / 4.2 / 4.6 TB/s of the weights that have to be read; the streams themselves run at 5.5 to
+// 5.9 TB/s, the rest is routing, the hand-over between the kernels and the last sums. mma.sync
 // kernels that converted the weights to bf16 in registers took 26 / 90 / 188 us, bound by
 // ~100 to 180 instructions per KB of weights and by latency.
 //   warp 0      TMA producer: 128 weight rows x 128 bytes of K per stage (128-byte swizzle).
@@ -29,7 +29,7 @@
 // Kernel 1: a unit is one expert's 64 gate and the matching 64 up rows (16 of each per warp
 // of the epilogue, one shuffle brings a pair together); units go round-robin over the CTAs.
 // h leaves as fp32 with the largest magnitude of every 16 of a row. Kernel 2: a CTA owns
-// 128 output columns and every split-th expert: the weighted rows are summed in shared
+// 128 output columns and every split-th group: the weighted rows are summed in shared
 // memory, and the CTAs of a column tile, one cluster's, add theirs in a fixed order through
 // distributed shared memory (no atomics on results: deterministic).
 // Both kernels know the whole routing: each cluster routes the tokens, a warp
