@@ -225,6 +225,25 @@ def test_gemm_swiglu_extremes():
         assert Y[m, 1] == 0
 
 
+@pytest.mark.parametrize("K", [16, 4096])
+@pytest.mark.parametrize("g", [-60.0, -88.5, -100.0, -150.0])
+def test_gemm_swiglu_small_gate_times_large_up(K, g):
+    """exp(g) below fp32's range, silu(g) * u well within it."""
+    W = torch.zeros(2, K, dtype=torch.int8, device="cuda")
+    W[0, :16], W[1, :16] = -127, 1
+    X = torch.full((3, K), 127, dtype=torch.int8, device="cuda")
+    u = 1e4 * 10.0 ** (-g / 2.5)
+    if u > 1e38:
+        u = 1e38
+    sw = torch.tensor([-g / (127 * 127 * 16), u / (127 * 16)], dtype=torch.float32, device="cuda")
+    Y = q.i8_gemm(W, sw, X, torch.ones(3, device="cuda"), act=q.ACT_SWIGLU)
+    gate, up = -127.0 * 127 * 16 * float(sw[0]), 127.0 * 16 * float(sw[1])
+    exact = gate * np.exp(gate) / (1 + np.exp(gate)) * up
+    # the gate's two roundings move the exponential by 2 * 2^-24 |g|, ex2 of half of it, squared, by
+    # 2 * (2 + 0.6 |g|) ulp of 2^-23; a few roundings more: below 2^-14 together; then bf16
+    assert (abs(Y.double().cpu() / exact - 1) <= 2.0 ** -8 + 2.0 ** -14).all()
+
+
 # ------------------------------------------------------------ refusals on the GPU
 
 def test_binding_refusals():
