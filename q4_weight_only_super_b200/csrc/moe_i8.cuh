@@ -198,8 +198,8 @@ __device__ __forceinline__ void mi8_route(const Mi8Params& p, Mi8Route<PL>& r, f
     mi8_topk<PL>(key, p.topk, lane, list, id, w);
     // softmax over the selected: lane j has the j-th, the sum in a fixed butterfly order
     const uint32_t k = w[min(lane, p.topk - 1)], k0 = w[0];
-    const float nan = __uint_as_float(0x7FC00000u);
-    const float v = k == 1u ? nan : key_value(k), v0 = k0 == 1u ? nan : key_value(k0);
+    // a NaN logit weighs nothing, as -inf does; with nothing but NaN, v0 is NaN
+    const float v = k == 1u ? -INFINITY : key_value(k), v0 = k0 == 1u ? __uint_as_float(0x7FC00000u) : key_value(k0);
     const float ek = lane < p.topk ? expf(v - v0) : 0.f;
     float den = ek;
 #pragma unroll

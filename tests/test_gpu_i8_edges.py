@@ -1,0 +1,44 @@
+"""The 8-bit integer lane at the edges of what its entry points accept."""
+import pytest
+import torch
+
+from tests.i8_bound import moe_ref_and_bound
+from tests.test_gpu_i8 import moe_inputs
+
+pytestmark = pytest.mark.gpu
+
+q = pytest.importorskip("q4_weight_only_super_b200")
+
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu(cuda_ok):
+    q.lib()
+    q.q4k_last_device_status()
+    yield
+    assert q.q4k_last_device_status() == 0
+
+
+def within(Y, *case, residual=None):
+    y, tol = moe_ref_and_bound(*case, residual=residual)
+    bad = ~((Y.to(F64) - y).abs() <= tol)  # (a NaN is bad)
+    assert not bad.any(), float(((Y.to(F64) - y).abs() / tol.clamp_min(1e-300)).max())
+
+
+# ------------------------------------------------- masked experts and NaN logits
+
+@pytest.mark.parametrize("E", [6, 140, 300])
+def test_moe_fewer_numbers_than_topk_among_the_logits(E):
+    """A NaN logit ranks below all others; selected for want of others it weighs nothing."""
+    L, Wg, sg, Wd, sd, X = moe_inputs(63, 4, E, 64, 48)
+    nan = float("nan")
+    L[0, 2:] = nan
+    L[1, :] = nan
+    L[1, E - 1] = -3.0
+    L[2, 1:] = nan
+    L[2, 3] = -float("inf")
+    L[3, 1] = float("inf")  # no softmax with it
+    Y = q.moe_i8_layer(L, 4, Wg, sg, Wd, sd, X)
+    within(Y[:3], L[:3], 4, Wg, sg, Wd, sd, X[:3])
+    assert torch.isnan(Y[3]).all()
