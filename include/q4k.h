@@ -360,7 +360,8 @@ q4k_status i8_gemm(const int8_t* W, const float* w_scale, const int8_t* X, const
  *   logits    fp32 [M][E]; routing as moe_route_permute (top-k by logit, equal logits to
  *             the lower id, softmax over the selected ones). A NaN logit ranks below all
  *             others and weighs nothing; a token whose logits are all -inf or NaN gets NaN,
- *             and so does one with a logit of +inf.
+ *             and so does one with a logit of +inf. An expert of weight 0 (masked by -inf,
+ *             and selected for want of others) adds nothing, whatever its scales hold.
  *   W_gate_up int8 [E][2F][H] (gate rows first), s_gate_up fp32 [E][2F];
  *   W_down    int8 [E][H][F], s_down fp32 [E][H];
  *   X         bf16 [M][H]; residual fp32 [M][H] or NULL, may be Y; Y fp32 [M][H]:

@@ -464,8 +464,11 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
         }
         if (DOWN) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (j + i < rows) ysum[r.row_token[row0 + j + i] * kI8Rows + 32 * q + lane] += r.row_weight[row0 + j + i] * y[i];
+          for (int i = 0; i < 4; ++i) {
+            // (a masked expert weighs 0 and stays out, whatever it holds: 0 times a NaN would not)
+            const float p_tj = j + i < rows ? r.row_weight[row0 + j + i] : 0.f;
+            if (p_tj != 0.f) ysum[r.row_token[row0 + j + i] * kI8Rows + 32 * q + lane] += p_tj * y[i];
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; i += 2) {

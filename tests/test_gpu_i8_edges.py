@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from tests.i8_bound import moe_ref_and_bound
-from tests.test_gpu_i8 import moe_inputs
+from tests.test_gpu_i8 import moe_inputs, scales
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,17 @@ def test_moe_fewer_numbers_than_topk_among_the_logits(E):
     Y = q.moe_i8_layer(L, 4, Wg, sg, Wd, sd, X)
     within(Y[:3], L[:3], 4, Wg, sg, Wd, sd, X[:3])
     assert torch.isnan(Y[3]).all()
+
+
+def test_moe_masked_expert_weighs_nothing_whatever_it_holds():
+    """An expert masked by -inf that is selected for want of others: its NaN scales, or an
+    overflow in its product, stay out of the token."""
+    L, Wg, sg, Wd, sd, X = moe_inputs(64, 5, 6, 64, 48)
+    L[:4, 2:] = -float("inf")
+    L[4] = torch.tensor([0.0, 1.0, -9.0, -9.0, -9.0, -9.0])
+    bg, bd = sg.clone(), sd.clone()
+    bg[2], bd[3] = float("nan"), float("inf")
+    bg[4], bd[5] = 1e30, float("nan")
+    within(q.moe_i8_layer(L, 4, Wg, bg, Wd, bd, X)[:4], L[:4], 4, Wg, sg, Wd, sd, X[:4])
+    # an expert that does weigh in brings its NaN
+    assert torch.isnan(q.moe_i8_layer(L, 4, Wg, bg, Wd, bd, X)[4]).all()
