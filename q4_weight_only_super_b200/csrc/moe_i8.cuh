@@ -283,6 +283,15 @@ __device__ __forceinline__ void mi8_digits(const float (&x)[4], float S, uint32_
   d[0] = __byte_perm(__byte_perm(v[0], v[1], 0x0062), __byte_perm(v[2], v[3], 0x0062), 0x5410);
 }
 
+// silu(g) * u = g u a^2 / (1 + h^2), h = exp(-|g| / 2), a = 1 or, g < 0, h. A row of h has a scale of
+// its own, so what counts is the product: exp(-|g|) is 0 or has lost bits from g = -87 down,
+// where a large u still makes a normal number of it; its half is whole down to g = -174.
+__device__ __forceinline__ float mi8_silu_mul(float g, float u) {
+  const float h = expf(-0.5f * fabsf(g));
+  const float a = g >= 0.f ? 1.f : h;
+  return g * (a * __frcp_rn(fmaf(h, h, 1.f))) * (a * u);
+}
+
 __device__ __forceinline__ float4 ld_cluster_f4(const float* p, uint32_t rank) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -473,7 +482,7 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
 #pragma unroll
           for (int i = 0; i < 4; i += 2) {
             const float got = __shfl_xor_sync(0xffffffffu, up ? y[i] : y[i + 1], 16);
-            const float hv = up ? silu_mul(got, y[i + 1]) : silu_mul(y[i], got);
+            const float hv = up ? mi8_silu_mul(got, y[i + 1]) : mi8_silu_mul(y[i], got);
             const int rj = j + i + (up ? 1 : 0);
             const bool in = rj < rows && f < p.F;
             uint32_t m = in ? __float_as_uint(hv) & 0x7FFFFFFFu : 0u;

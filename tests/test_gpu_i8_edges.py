@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from tests.i8_bound import moe_ref_and_bound
-from tests.test_gpu_i8 import moe_inputs, scales
+from tests.test_gpu_i8 import moe_inputs, _gen
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,22 @@ def test_moe_masked_expert_weighs_nothing_whatever_it_holds():
     within(q.moe_i8_layer(L, 4, Wg, bg, Wd, bd, X)[:4], L[:4], 4, Wg, sg, Wd, sd, X[:4])
     # an expert that does weigh in brings its NaN
     assert torch.isnan(q.moe_i8_layer(L, 4, Wg, bg, Wd, bd, X)[4]).all()
+
+
+# --------------------------------------------------------- gates far below zero
+
+@pytest.mark.parametrize("g,u", [(-60.0, 1e3), (-86.0, 1e6), (-95.0, 1e12), (-103.0, 1e16), (-110.0, 1e20),
+                                 (-150.0, 1e38)])
+def test_moe_gates_far_below_zero(g, u):
+    """exp(g) below fp32's range in a whole row of h, h itself well within it."""
+    L, Wg, sg, Wd, sd, X = moe_inputs(65, 3, 2, 32, 48)
+    F = 48
+    Wg[:] = 0
+    X[:, 3] = 1.0
+    Wg[:, :F, 3], Wg[:, F:, 3] = -127, 127
+    sg[:, :F], sg[:, F:] = -g / 127 * (1 + 0.01 * torch.rand(F, generator=_gen(1), device="cuda")), u / 127
+    sd[:] = 1e20
+    case = (L, 1, Wg, sg, Wd, sd, X)
+    Y = q.moe_i8_layer(*case)
+    assert torch.count_nonzero(Y) > 0
+    within(Y, *case)
