@@ -347,7 +347,8 @@ q4k_status i8_quantize(const uint16_t* X, int M, int K, int8_t* Q, float* scale,
  *   W int8 [N][K], w_scale fp32 [N], X int8 [M][K], x_scale fp32 [M]; codes -128..127.
  *   act == Q4K_ACT_NONE:   Y [M][N], fp32, or bf16 (nearest even) when out_bf16 != 0.
  *   act == Q4K_ACT_SWIGLU: Y bf16 [M][N/2] (out_bf16 must be set), SiLU(g) * u with
- *     g = y of rows 0..N/2-1 of W, u = y of rows N/2..N-1.
+ *     g = y of rows 0..N/2-1 of W, u = y of rows N/2..N-1; before the rounding to bf16
+ *     off by less than 2^-15 of its value for |g| < 90, 2^-14 beyond (normal numbers).
  * The sums are exact, so a result does not depend on the batch or the launch shape.
  * K <= 131056 (the sums fit int32); M and N up to 2^31 - 1024. M == 0 or N == 0 is a
  * no-op. */

@@ -125,9 +125,12 @@ __device__ __forceinline__ void tma2_load_gate_up(uint32_t dst, const CUtensorMa
 }
 
 // silu(g) * u = g u a^2 / (1 + h^2), h = exp(-|g| / 2), a = 1 or, g < 0, h: for a result that is
-// rounded to bf16. The exponential by ex2 is off by 2 + 0.6 |g| ulp (2^-23), the reciprocal (of
-// 1 to 2) by 1: together below 2^-16 of the result for |g| < 90. By halves, exp(-|g|)
-// does not leave fp32's range before silu(g) does. (With expf, tokens and 64-bit offsets one by
+// rounded to bf16. The argument of ex2 is off by |g| 2^-24, ex2 by 2^-22 and, below the normal
+// numbers, half a step of 2^-149, the reciprocal (of 1 to 2) by 2^-23; h enters twice: together
+// below (|g| + 8) 2^-22 of the result, 2^-15 for |g| < 90 and 2^-14 wherever the result is a normal
+// number. That is down to g = -181, u being large: by halves, the exponential does not leave
+// fp32's range before, as long as ex2 keeps subnormal results (flushing them saved nothing:
+// 512 x 34816 x 5120 67.5 us both ways). (With expf, tokens and 64-bit offsets one by
 // one, the epilogue of 128 x 256 sums took 12 us, longer than the MMAs of 5120 in K.)
 // V of them at once, step by step: their latencies overlap.
 template <int V>
@@ -135,7 +138,7 @@ __device__ __forceinline__ void i8_silu_mul(const float (&g)[V], const float (&u
   float h[V], r[V];
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(h[i]) : "f"(fabsf(g[i]) * -0.72134752f));  // -log2(e) / 2
+    asm volatile("ex2.approx.f32 %0, %1;" : "=f"(h[i]) : "f"(fabsf(g[i]) * -0.72134752f));  // -log2(e) / 2
 #pragma unroll
   for (int i = 0; i < V; ++i) asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[i]) : "f"(fmaf(h[i], h[i], 1.f)));
 #pragma unroll

@@ -1,4 +1,6 @@
 """The 8-bit integer lane at the edges of what its entry points accept."""
+import math
+
 import pytest
 import torch
 
@@ -59,6 +61,25 @@ def test_moe_masked_expert_weighs_nothing_whatever_it_holds():
 
 
 # --------------------------------------------------------- gates far below zero
+
+@pytest.mark.parametrize("K", [16, 4096])
+@pytest.mark.parametrize("g", [-165.0, -174.0, -176.0, -178.0, -180.0])
+def test_gemm_swiglu_gate_far_below_zero(K, g):
+    """u near the largest there is: silu(g) * u is a normal number down to g = -181."""
+    W = torch.zeros(2, K, dtype=torch.int8, device="cuda")
+    W[0, :16], W[1, :16] = -127, 1
+    X = torch.full((3, K), 127, dtype=torch.int8, device="cuda")
+    sw = torch.tensor([-g / (127 * 127 * 16), 3.3e38 / (127 * 16)], dtype=torch.float32, device="cuda")
+    Y = q.i8_gemm(W, sw, X, torch.ones(3, device="cuda"), act=q.ACT_SWIGLU)
+    gate, up = -127.0 * 127 * 16 * float(sw[0]), 127.0 * 16 * float(sw[1])
+    exact = gate * math.exp(gate) / (1 + math.exp(gate)) * up
+    assert abs(exact) > 2.0 ** -126
+    # the gate's two roundings move the exponential by 2 * 2^-24 |g|; that of half the gate is off by
+    # (|g| + 8) * 2^-22 squared, and, below the normal numbers, by half a step of 2^-149, as the
+    # product with the reciprocal is: of 2^-130 at least, 2^-20 each, the first squared; then bf16
+    tol = 2.0 ** -8 + abs(gate) * 2.0 ** -23 + (abs(gate) + 8) * 2.0 ** -22 + 3 * 2.0 ** -20
+    assert (abs(Y.double().cpu() / exact - 1) <= 1.01 * tol).all()
+
 
 @pytest.mark.parametrize("g,u", [(-60.0, 1e3), (-86.0, 1e6), (-95.0, 1e12), (-103.0, 1e16), (-110.0, 1e20),
                                  (-150.0, 1e38)])
