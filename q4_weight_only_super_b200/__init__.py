@@ -371,9 +371,12 @@ def _need(fn, name, t, dtypes, shape, dev):
                      f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _two_dims(fn, name, t):
-    if t.dim() != 2:
-        raise ValueError(f"{fn}: {name} must have two dimensions; got shape {tuple(t.shape)}")
+def _dims(fn, name, t, n):
+    """The n sizes of an operand; they are passed on as int, which would cut a larger one off."""
+    if t.dim() != n:
+        raise ValueError(f"{fn}: {name} must have {'two' if n == 2 else 'three'} dimensions; got shape {tuple(t.shape)}")
+    if max(t.shape) > 0x7fffffff:
+        raise ValueError(f"{fn}: {name} has a size beyond 2^31 - 1: {tuple(t.shape)}")
     return t.shape
 
 
@@ -394,7 +397,7 @@ def _empty(shape, dtype, dev, stream):
 def i8_quantize(X, Q=None, scale=None, stream=None):
     """bf16 rows X [M][K] -> (int8 codes [M][K], fp32 scales [M]); see include/q4k.h."""
     fn, dev = "i8_quantize", X.get_device()
-    shape = M, K = _two_dims(fn, "X", X)
+    shape = M, K = _dims(fn, "X", X, 2)
     _need(fn, "X", X, _BF16, shape, dev)
     if Q is None:
         Q = _empty((M, K), torch.int8, dev, stream)
@@ -423,12 +426,13 @@ def i8_gemm(W, w_scale, X, x_scale, act: int = ACT_NONE, out_bf16: bool = False,
     # one pass over what has to hold (a fifth of a small call's time); which of it does not is
     # found out only then
     if not (len(shape) == len(x_shape) == 2 and shape[1] == x_shape[1]
+            and shape[0] <= 0x7fffffff >= shape[1] and x_shape[0] <= 0x7fffffff
             and W.dtype is X.dtype is _int8 and w_scale.dtype is x_scale.dtype is _float32
             and w_scale.shape == shape[:1] and x_scale.shape == x_shape[:1]
             and dev == X.get_device() == w_scale.get_device() == x_scale.get_device() >= 0
             and W.is_contiguous() and X.is_contiguous() and w_scale.is_contiguous() and x_scale.is_contiguous()):
-        N, K = _two_dims("i8_gemm", "W", W)
-        M = _two_dims("i8_gemm", "X", X)[0]
+        N, K = _dims("i8_gemm", "W", W, 2)
+        M = _dims("i8_gemm", "X", X, 2)[0]
         _need("i8_gemm", "W", W, _I8, (N, K), dev)
         _need("i8_gemm", "w_scale", w_scale, _F32, (N,), dev)
         _need("i8_gemm", "X", X, _I8, (M, K), dev)
@@ -456,10 +460,10 @@ def moe_i8_layer(logits, topk: int, W_gate_up, s_gate_up, W_down, s_down, X, res
     (see include/q4k.h): logits fp32 [M][E], W_gate_up int8 [E][2F][H], W_down int8 [E][H][F]
     with fp32 scales [E][2F] and [E][H], X bf16 [M][H]; returns Y fp32 [M][H]."""
     fn, dev = "moe_i8_layer", W_gate_up.get_device()
-    M, E = _two_dims(fn, "logits", logits)
-    if W_down.dim() != 3:
-        raise ValueError(f"{fn}: W_down must have three dimensions; got shape {tuple(W_down.shape)}")
-    _, H, F = W_down.shape
+    M, E = _dims(fn, "logits", logits, 2)
+    _, H, F = _dims(fn, "W_down", W_down, 3)
+    if topk > 0x7fffffff:
+        raise ValueError(f"{fn}: topk {topk} is beyond 2^31 - 1")
     _need(fn, "logits", logits, _F32, (M, E), dev)
     _need(fn, "W_gate_up", W_gate_up, _I8, (E, 2 * F, H), dev)
     _need(fn, "s_gate_up", s_gate_up, _F32, (E, 2 * F), dev)

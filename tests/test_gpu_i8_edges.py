@@ -96,3 +96,15 @@ def test_moe_gates_far_below_zero(g, u):
     Y = q.moe_i8_layer(*case)
     assert torch.count_nonzero(Y) > 0
     within(Y, *case)
+
+
+# ----------------------------------------------------------------- large sizes
+
+def test_k_beyond_int_is_refused():
+    """Passed on as int, 2^32 + 32 would be 32."""
+    K = 2 ** 32 + 32
+    W, one = torch.zeros(1, K, dtype=torch.int8, device="cuda"), torch.ones(1, device="cuda")
+    with pytest.raises(ValueError, match="2\\^31"):
+        q.i8_gemm(W, one, W, one)
+    with pytest.raises(ValueError, match="2\\^31"):
+        q.i8_quantize(torch.zeros(1, K, dtype=torch.bfloat16, device="cuda"))
