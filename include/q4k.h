@@ -409,6 +409,14 @@ q4k_status q4k_last_device_status(void* stream);
  * Returns Q4K_ERR_CUDA if the copy fails. */
 q4k_status q4k_test_wait_fault(int drop_stage, uint64_t wait_limit_ns);
 
+/* Test hook: the form in which i8_gemm computes a product of these sizes, so that a test can
+ * tell which of its kernels it ran. Nothing is launched. The form depends on the device:
+ *   sms, fit  a device of sms SMs on which fit[c] clusters of c CTAs (c = 1..8; fit[0] is not
+ *             read) are resident at once; sms == 0: the current device.
+ *   cut       7 ints: 1 for CTA pairs, CTAs per SM, token tiles, tokens per tile, tiles (a
+ *             pair's are twice as high) along W's rows, shares of K, stages of the ring. */
+q4k_status q4k_test_i8_cut(int M, int N, int K, int act, int sms, const int* fit, int* cut);
+
 /* Static description of a status code. */
 const char* q4k_status_string(int status);
 

@@ -19,7 +19,7 @@ __all__ = [
     "moe_route_permute_noalloc", "moe_route_permute_hidden", "moe_route_gate_up",
     "moe_q4k_grouped", "moe_combine", "moe_combine_residual", "q4k_workspace_bytes", "q4k_last_device_status",
     "i8_quantize", "i8_gemm", "moe_i8_layer",
-    "q4k_test_wait_fault",
+    "q4k_test_wait_fault", "q4k_test_i8_cut",
     "ACT_NONE", "ACT_SWIGLU", "OP_GEMM", "OP_ROUTE", "OP_GROUPED", "OP_GEMV", "OP_MOE_I8", "EXPORTS",
 ]
 
@@ -55,6 +55,7 @@ EXPORTS = {
     "q4k_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "q4k_last_device_status": (_i, [_p]),
     "q4k_test_wait_fault": (_i, [_i, ctypes.c_uint64]),
+    "q4k_test_i8_cut": (_i, [_i, _i, _i, _i, _i, ctypes.POINTER(_i), ctypes.POINTER(_i)]),
     "q4k_status_string": (ctypes.c_char_p, [_i]),
 }
 
@@ -501,3 +502,11 @@ def q4k_test_wait_fault(drop_stage: int = -1, wait_limit_ns: int = 0) -> None:
     """Test hook: make the weight producers skip stage `drop_stage` (-1: off) and set the
     bounded-wait limit (0: the 2 s default). Synchronous; see include/q4k.h."""
     _check("q4k_test_wait_fault", lib().q4k_test_wait_fault(int(drop_stage), int(wait_limit_ns)))
+
+
+def q4k_test_i8_cut(M: int, N: int, K: int, act: int = ACT_NONE, sms: int = 0, fit=None) -> dict:
+    """Test hook: the form in which i8_gemm computes a product of these sizes, on the current
+    device or on one of `sms` SMs with room for fit[c] clusters of c CTAs; see include/q4k.h."""
+    cut = (_i * 7)()
+    _check("q4k_test_i8_cut", lib().q4k_test_i8_cut(M, N, K, act, sms, None if fit is None else (_i * 9)(*fit), cut))
+    return dict(zip(("pair", "ctas_per_sm", "m_tiles", "nt", "n_tiles", "ksplit", "stages"), cut))

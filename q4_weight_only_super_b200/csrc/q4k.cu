@@ -497,7 +497,9 @@ struct I8Cut {
 // every cut of each measured, and mean nothing beyond that: the chosen cut is 1.5% slower than
 // the fastest in the mean, 10% at most (250 x 30000 x 512: 13.3 for 12.0 us; 37 x 2051 x 2064:
 // 5.7 for 5.4).
-I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
+// fit(c): clusters of c CTAs resident at once, one CTA per SM.
+template <typename Fit>
+I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms, Fit fit) {
   const int nk = (K + kI8KB - 1) / kI8KB;
   const double dram = ((double)rows * (kI8Rows / tile_rows) + M) * K / 3310.;
   I8Cut best = {};
@@ -524,7 +526,7 @@ I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms) {
         const double ctas = tiles * P * ks;
         if (ks > 1) {
           const int per = ((c.nt + ks - 1) / ks + 3) / 4 * 4;
-          if (tiles > (double)i8_cluster_fit(P * ks) * (1 + c.halved)) continue;
+          if (tiles > (double)fit(P * ks) * (1 + c.halved)) continue;
           if ((size_t)ks * kI8Rows * per * 4 > c.stages * stage) continue;
         }
         const double waves = std::ceil(ctas / (sms * (1 + c.halved)));
@@ -573,7 +575,7 @@ I8Plan* i8_plan(int M, int N, int K, bool swiglu, const void* W, const void* X, 
                : nullptr;
   const int rows = swiglu ? N / 2 : N;
   e.M = 0;  // (not a plan, until it is whole)
-  e.cut = i8_cut(M, rows, swiglu ? kI8Rows / 2 : kI8Rows, K, sms);
+  e.cut = i8_cut(M, rows, swiglu ? kI8Rows / 2 : kI8Rows, K, sms, i8_cluster_fit);
   e.boxed = swiglu && rows % 16 == 0;
   if (!(e.boxed ? make_tmap_gate_up(&e.tw, W, 1, rows, K) : make_tmap_i8(&e.tw, W, N, K, swiglu ? 16 : kI8Rows)) ||
       !make_tmap_i8(&e.tx, X, M, K, e.cut.nt / (1 + e.cut.pair)))
@@ -1256,6 +1258,20 @@ q4k_status moe_route_permute_hidden(const uint16_t* X, const uint16_t* W_router,
   }
   return moe_route_permute(logits, M, E, topk, topk_ids, topk_w, expert_offsets, perm, inv_perm, row_token, ws,
                            ws_bytes, stream);
+}
+
+q4k_status q4k_test_i8_cut(int M, int N, int K, int act, int sms, const int* fit, int* cut) {
+  if (M <= 0 || N <= 0 || K <= 0 || K % 16 || (act == Q4K_ACT_SWIGLU && N % 2)) return Q4K_ERR_SHAPE;
+  if ((act != Q4K_ACT_NONE && act != Q4K_ACT_SWIGLU) || K > kI8MaxK || M > kI8MaxRows || N > kI8MaxRows)
+    return Q4K_ERR_UNSUPPORTED;
+  if (!cut || (sms > 0 && !fit)) return Q4K_ERR_NULL;
+  const int rows = act == Q4K_ACT_SWIGLU ? N / 2 : N, tile_rows = act == Q4K_ACT_SWIGLU ? kI8Rows / 2 : kI8Rows;
+  if (sms <= 0 && sm_count() <= 0) return Q4K_ERR_CUDA;
+  const I8Cut c = i8_cut(M, rows, tile_rows, K, sms > 0 ? sms : sm_count(),
+                         [&](int n) { return sms > 0 ? fit[n] : i8_cluster_fit(n); });
+  const int out[7] = {c.pair, 1 + c.halved, c.m_tiles, c.nt, c.n_tiles, c.ksplit, c.stages};
+  std::copy(out, out + 7, cut);
+  return Q4K_OK;
 }
 
 q4k_status q4k_test_wait_fault(int drop_stage, uint64_t wait_limit_ns) {
