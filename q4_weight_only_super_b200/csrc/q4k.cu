@@ -512,7 +512,7 @@ I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms, Fit fit) {
       c.pair = pair;
       c.halved = form & 1;
       c.m_tiles = mt;
-      c.nt = ((M + mt - 1) / mt + grain - 1) / grain * grain;
+      c.nt = ((int)(((int64_t)M + mt - 1) / mt) + grain - 1) / grain * grain;  // (M + mt may pass 2^31)
       if (c.nt > kI8MaxNT) continue;
       c.n_tiles = (rows + tile_rows * P - 1) / (tile_rows * P);
       const size_t stage = kI8ATile + (size_t)(c.nt / P) * kI8KB;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests.i8_bound import moe_ref_and_bound
-from tests.test_gpu_i8 import moe_inputs, _gen
+from tests.test_gpu_i8 import codes, moe_inputs, scales, _gen
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,23 @@ def test_k_beyond_int_is_refused():
         q.i8_gemm(W, one, W, one)
     with pytest.raises(ValueError, match="2\\^31"):
         q.i8_quantize(torch.zeros(1, K, dtype=torch.bfloat16, device="cuda"))
+
+
+def test_gemm_most_tokens():
+    """M at its limit: 34 GB of codes, in rows that repeat every 1024 under scales that do not."""
+    M, K = 2 ** 31 - 1024, 16
+    if torch.cuda.mem_get_info()[0] < 70 * 2 ** 30:
+        pytest.skip("not enough free memory")
+    g = _gen(70)
+    W, sw, block = codes(g, 1, K), scales(g, 1), codes(g, 1024, K)
+    X = torch.empty(M, K, dtype=torch.int8, device="cuda")
+    X.view(-1, 1024, K).copy_(block.expand(M // 1024, 1024, K))
+    sx = torch.empty(M, device="cuda")
+    sx.view(-1, 1024).copy_((1 + torch.arange(M // 1024, device="cuda") % 4093 / 4096).expand(1024, -1).t())
+    Y = q.i8_gemm(W, sw, X, sx)
+    acc = (block.to(F64) @ W.to(F64).T).to(torch.float32)[:, 0]
+    for c in range(0, M // 1024, 1 << 16):
+        rows = slice(1024 * c, 1024 * (c + (1 << 16)))
+        assert torch.equal(Y[rows].view(-1, 1024), acc * sx[rows].view(-1, 1024) * sw)
+    del X, sx, Y
+    torch.cuda.empty_cache()

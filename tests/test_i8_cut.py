@@ -52,3 +52,20 @@ def test_hook_refusals(q):
             q.q4k_test_i8_cut(M, N, K, act, 148, FITS[0])
     with pytest.raises(q.Q4KError):
         q.q4k_test_i8_cut(4, 32, 64, 0, 148, None)
+
+
+@pytest.mark.parametrize("M", [2 ** 31 - 1024, 2 ** 31 - 1025, 2139130000, 2 ** 31 - 2 ** 24])
+@pytest.mark.parametrize("N,K,act", [(1, 16, 0), (4, 16, 1), (100, 144, 0)])
+@pytest.mark.parametrize("fit", FITS)
+def test_cuts_of_the_most_tokens(q, M, N, K, act, fit):
+    c = check(q, M, N, K, act, fit)
+    # the first token of every tile, and of a pair's second half of it, stays an int
+    assert (c["m_tiles"] - 1) * c["nt"] + c["nt"] // 2 < 2 ** 31
+
+
+@pytest.mark.parametrize("N", [2 ** 31 - 1024, 2 ** 31 - 1026])
+@pytest.mark.parametrize("act", [0, 1])
+def test_cuts_of_the_most_channels(q, N, act):
+    for M in (1, 300):
+        c = check(q, M, N, 16, act, FITS[0])
+        assert c["n_tiles"] * (1 + c["pair"]) * 128 < 2 ** 31
