@@ -1,11 +1,12 @@
-"""The 8-bit integer lane at the edges of what its entry points accept."""
+"""moe_i8_layer within the bound that its number formats allow, and the 8-bit lane at the edges
+of what its entry points accept: masked experts, NaN logits, gates far below zero."""
 import math
 
 import pytest
 import torch
 
 from tests.i8_bound import moe_ref_and_bound
-from tests.test_gpu_i8 import codes, moe_inputs, scales, _gen
+from tests.test_gpu_i8 import MOE, codes, moe_inputs, scales, _gen
 
 pytestmark = pytest.mark.gpu
 
@@ -26,6 +27,36 @@ def within(Y, *case, residual=None):
     y, tol = moe_ref_and_bound(*case, residual=residual)
     bad = ~((Y.to(F64) - y).abs() <= tol)  # (a NaN is bad)
     assert not bad.any(), float(((Y.to(F64) - y).abs() / tol.clamp_min(1e-300)).max())
+
+
+# ------------------------------------------------------------ the layer's precision
+
+@pytest.mark.parametrize("M,E,topk,H,F", MOE + [(32, 128, 8, 2048, 768), (32, 300, 16, 144, 80), (32, 40, 16, 1040, 208),
+                                                (3, 5, 2, 32, 3104), (29, 1024, 11, 64, 48), (6, 20, 4, 4096, 6400)])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_moe_keeps_24_bits(M, E, topk, H, F, with_residual):
+    L, Wg, sg, Wd, sd, X = moe_inputs(M + 7 * E + H, M, E, H, F)
+    R = 0.01 * torch.randn(M, H, generator=_gen(9), device="cuda") if with_residual else None
+    within(q.moe_i8_layer(L, topk, Wg, sg, Wd, sd, X, residual=R), L, topk, Wg, sg, Wd, sd, X, residual=R)
+
+
+def test_moe_rows_of_wide_range_keep_24_bits():
+    """A few activations thousands of times the others."""
+    L, Wg, sg, Wd, sd, X = moe_inputs(61, 9, 8, 1024, 256)
+    X[:, ::97] *= 3000
+    X[2, 5] *= 1e6
+    sg = sg / 300
+    within(q.moe_i8_layer(L, 3, Wg, sg, Wd, sd, X), L, 3, Wg, sg, Wd, sd, X)
+
+
+def test_moe_tokens_do_not_touch_each_other():
+    """With the routing as it is, other tokens' values change nothing, across groups of 8 rows."""
+    L, Wg, sg, Wd, sd, X = moe_inputs(62, 32, 4, 320, 144)
+    Y = q.moe_i8_layer(L, 2, Wg, sg, Wd, sd, X)
+    X2 = X.clone()
+    X2[1::2] *= torch.tensor([1e4, -1e-6, 0.0, 1e12] * 4, device="cuda")[:, None].to(torch.bfloat16)
+    Y2 = q.moe_i8_layer(L, 2, Wg, sg, Wd, sd, X2)
+    assert torch.equal(Y2[::2], Y[::2]) and not torch.equal(Y2[1::2], Y[1::2])
 
 
 # ------------------------------------------------- masked experts and NaN logits
