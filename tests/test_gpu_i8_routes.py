@@ -129,3 +129,21 @@ def test_pairs_on_two_streams_and_replayed():
     graph.replay()
     for a, y in zip(args, ys):
         assert torch.equal(y, gemm_ref32(a[0], a[1], a[2], a[3]))
+
+
+@pytest.mark.parametrize("M,N,K,act", [(605, 20980, 304, 0), (457, 25752, 320, 1), (271, 3486, 4240, 0), (1499, 832, 3120, 1)])
+def test_waits_of_pairs_run_out_and_recover(M, N, K, act):
+    """A stage that never arrives: pairs at two CTAs per SM, walking and splitting K."""
+    assert form(M, N, K, act)[0] == 1
+    g = _gen(5)
+    args = (codes(g, N, K), scales(g, N) / 100, codes(g, M, K), scales(g, M))
+    good = q.i8_gemm(*args, act=act)
+    assert q.q4k_last_device_status() == 0
+    try:
+        q.q4k_test_wait_fault(0, 200_000)  # every producer skips its first stage; 200 us limit
+        q.i8_gemm(*args, act=act)
+        assert q.q4k_last_device_status() == 7  # Q4K_ERR_DEVICE_TIMEOUT
+    finally:
+        q.q4k_test_wait_fault(-1, 0)
+    assert torch.equal(q.i8_gemm(*args, act=act), good)
+    assert q.q4k_last_device_status() == 0
