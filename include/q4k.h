@@ -396,10 +396,10 @@ q4k_status q4k_last_device_status(void* stream);
 /* Test hook for the bounded device-side waits (failure detection without a GPU
  * fault; hipEngine 0.3.0 README, "Core principles": fail closed instead of
  * hanging or falling back). Sets, for every later launch on the current device:
- *   drop_stage     >= 0: the weight producer of every CTA of q4k_gemm and of the
- *                  decode GEMVs skips its stage with this index (no copy, no
- *                  arrival), so the roles waiting for it reach the wait limit;
- *                  < 0: off (the default).
+ *   drop_stage     >= 0: the weight producer of every CTA of q4k_gemm, of the
+ *                  decode GEMVs, of i8_gemm and of moe_i8_layer skips its stage
+ *                  with this index (no copy, no arrival), so the roles waiting
+ *                  for it reach the wait limit; < 0: off (the default).
  *   wait_limit_ns  the limit of every bounded wait, in ns; 0 restores the
  *                  default (2 s).
  * A kernel whose wait expires latches Q4K_ERR_DEVICE_TIMEOUT, stops every role,

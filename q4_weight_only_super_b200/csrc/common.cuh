@@ -20,9 +20,9 @@ __device__ int g_status;
 // far beyond any legal wait. A test may shorten it (q4k_test_wait_fault).
 __device__ unsigned long long g_wait_limit_ns = 2000000000ull;
 // Test hook (q4k_test_wait_fault): when >= 0, the weight producer of every CTA of the
-// prefill GEMM and the decode GEMVs skips its stage with this index -- neither the
-// copy nor the arrival happens -- so the roles waiting for that stage run into the
-// wait limit. -1 (the default) disables it.
+// prefill GEMM, the decode GEMVs, the int8 product and both kernels of the int8 expert
+// layer skips its stage with this index -- neither the copy nor the arrival happens -- so
+// the roles waiting for that stage run into the wait limit. -1 (the default) disables it.
 __device__ int g_test_drop_stage = -1;
 
 __device__ __forceinline__ void latch_status(int code) { atomicCAS(&g_status, 0, code); }

@@ -26,10 +26,12 @@
 // SPLIT: with too few tiles for the GPU the CTAs (or pairs) of a cluster split K: every CTA
 // sends each other one of its share of the token columns through distributed shared
 // memory, and sums and stores its own share.
-// Measured: 17408 x 5120 at 4096 tokens 246 us (2.97 POPS at the 1.6 GHz that the power cap
-// leaves, tensor pipe 80% busy; lone CTAs 279); 34816 x 5120 with SwiGLU at 512 tokens 70 us
-// (2.6 POPS), at one token 30.3 us (5.9 TB/s, 90% of the measured copy rate); 5120 x 17408 at
-// eight tokens 18.3 us (split over six CTAs; unsplit 40), at 300 tokens 29.7 us.
+// Measured, in graphs of a few calls: 17408 x 5120 at 4096 tokens 245 us (2.98 POPS at the 1.6 GHz
+// that the power cap leaves, tensor pipe 80% busy; lone CTAs 279); 34816 x 5120 with SwiGLU at 512
+// tokens 68 us (2.7 POPS), at one token 29.5 us (6.0 TB/s, 92% of the measured copy rate); 5120 x
+// 17408 at eight tokens 18.1 us (split over six CTAs; unsplit 40), at 300 tokens 29.7 us. Called one
+// after the other for longer, the power cap lowers the clock of the products that keep the
+// tensor pipe busy: 285, 80 and 34 us at 4096, 512 and 300 tokens.
 // SwiGLU tiles hold 64 gate and the matching 64 up rows, 16 of each per warp's 32 lanes, so
 // that one shuffle brings a gate and its up value together.
 // Every wait is bounded; on expiry the kernel latches Q4K_ERR_DEVICE_TIMEOUT, stops all

@@ -15,8 +15,8 @@
 // That keeps what fp32 sums would (X: S is a power of two, so a bf16 value within 2^14 of
 // its row's largest is exact; h: to 2^-23 of its row's largest), costs no instruction per
 // weight, and makes the sums independent of their order.
-// Measured (128 experts, top-8, H = 2048, F = 768): 19.7 / 58.8 / 115 us for 1 / 8 / 32 tokens,
-// 1.9 / 4.2 / 4.6 TB/s of the weights that have to be read; the streams themselves run at 5.5 to
+// Measured (128 experts, top-8, H = 2048, F = 768): 19.9 / 59.5 / 115 us for 1 / 8 / 32 tokens,
+// 1.9 / 4.1 / 4.6 TB/s of the weights that have to be read; the streams themselves run at 5.5 to
 // 5.9 TB/s, the rest is routing, the hand-over between the kernels and the last sums. mma.sync
 // kernels that converted the weights to bf16 in registers took 26 / 90 / 188 us, bound by
 // ~100 to 180 instructions per KB of weights and by latency.

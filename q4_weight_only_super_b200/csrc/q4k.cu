@@ -494,9 +494,9 @@ struct I8Cut {
 // come from DRAM at 3310 bytes a cycle, and the smaller of the two is not hidden by the larger
 // altogether. Then the epilogue, of a K split with its exchange, and a pair's hand-shakes. The
 // constants are fitted to 38 shapes (1 .. 3000 tokens, 200 .. 34816 channels, K 512 .. 17408),
-// every cut of each measured, and mean nothing beyond that: the chosen cut is 1.5% slower than
-// the fastest in the mean, 10% at most (250 x 30000 x 512: 13.3 for 12.0 us; 37 x 2051 x 2064:
-// 5.7 for 5.4).
+// every cut of each measured, and mean nothing beyond that: on these shapes the chosen cut is 1.5%
+// slower than the fastest in the mean, 11% at most (250 x 30000 x 512: 13.3 for 12.0 us). On
+// others the cuts were not measured against each other.
 // fit(c): clusters of c CTAs resident at once, one CTA per SM.
 template <typename Fit>
 I8Cut i8_cut(int M, int rows, int tile_rows, int K, int sms, Fit fit) {
