@@ -370,8 +370,8 @@ q4k_status i8_gemm(const int8_t* W, const float* w_scale, const int8_t* X, const
  *     h = SiLU(g) * u, g and u = s_gate_up * (W_gate_up[e] X[t]).
  * No 8-bit rounding inside: X and h (fp32) enter the integer products as 24-bit fixed
  * point with one scale per row (X: a power of two, so a value within 2^14 of its row's
- * largest is exact; h: to 2^-23 of its row's largest, or of 2^-100), their sums exact, and
- * the combine is summed in fp32 in an order that depends on the sizes and the routing
+ * largest, or of 2^-105, is exact, others to 2^-22 of it; h: to 2^-23 of its row's largest,
+ * or of 2^-100), their sums exact, and the combine is summed in fp32 in an order that depends on the sizes and the routing
  * alone. A token whose X holds an infinity or a NaN gets NaN.
  *   ws/ws_bytes: device scratch of q4k_workspace_bytes(Q4K_OP_MOE_I8, M, H, F, E, topk)
  *   bytes; calls (and captured graphs) that share it must be ordered on one stream.
