@@ -170,6 +170,14 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
 }
+__device__ __forceinline__ void st_release_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.release.cluster.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_acquire_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.acquire.cluster.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ void st_cluster_s32(uint32_t addr, int32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -225,6 +233,8 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
   auto bar_tempty = [&](int a) { return bars + 8u * (2 * kI8MaxStages + 2 + a); };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + p.tail + 8 * (2 * kI8MaxStages + 4));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + p.tail + 8 * (2 * kI8MaxStages + 4) + 4);
+  const uint32_t bar_done = bars + 8u * (2 * kI8MaxStages + 5);    // issued MMAs have ended (on expiry)
+  const uint32_t odd_issued = bars + 8u * (2 * kI8MaxStages + 6);  // stages that a pair's odd CTA has issued, plus 1
   float* s_xs = reinterpret_cast<float*>(smem + p.tail + 256);  // [epilogue warps][nt] token scales
 
   // place in the cluster: ranks P s + r: half r of the pair, share s of K
@@ -242,7 +252,9 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
       mbar_init(bar_tfull(a), 1);
       mbar_init(bar_tempty(a), P * kI8EpiWarps);
     }
+    mbar_init(bar_done, 1);
     *abort_flag = 0;
+    if (PAIR) asm volatile("st.shared::cta.u32 [%0], %1;" ::"r"(odd_issued), "r"(0u) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -280,20 +292,20 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
   auto tile_m0 = [&](int tile) { return tile % p.m_tiles * p.nt; };
   auto tile_n = [&](int tile) { return tile / p.m_tiles * P + r; };
 
+  int issued = 0;  // by a role's one thread: stages copied (warp 0), consumed (warp 1)
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (lane == 0) {
       const int drop = g_test_drop_stage;  // test hook; -1 in normal use
-      int it = 0;
       I8Ring at;
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += step) {
         const int m0 = tile_m0(tile) + r * (p.nt / P), nti = tile_n(tile);
-        for (int k = 0; k < nk; ++k, ++it, at.next(p.stages)) {
+        for (int k = 0; k < nk; ++k, ++issued, at.next(p.stages)) {
           const int s = at.s;
           // (a barrier's phase before its first counts as complete)
           if (!(ok = mbar_wait_l(bar_empty(s), at.parity ^ 1, abort_flag, limit))) break;
-          if (it == drop) continue;  // test hook: this stage never arrives
+          if (issued == drop) continue;  // test hook: this stage never arrives
           if (r == 0) mbar_arrive_expect_tx(bar_full(s), P * stage_bytes);
           const uint32_t a_dst = sbase + s * stage_bytes;
           const uint32_t bar = PAIR ? cluster_addr(bar_full(s), leader) : bar_full(s);
@@ -322,13 +334,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
           load(a_dst + kI8ATile, &tmap_x, m0);
         }
       }
-      // every issued stage lands before this CTA may exit (on the normal path the MMA
-      // role has waited for all of them; of a pair, the even CTA's barriers tell)
-      if (*abort_flag && r == 0) {
-        I8Ring back;
-        for (int i = 0; i < it; ++i, back.next(p.stages))
-          if (i >= it - p.stages && i != drop) mbar_wait_drain(bar_full(back.s), back.parity);
-      }
+      if (PAIR && r == 1) st_release_cluster_u32(cluster_addr(odd_issued, leader), (uint32_t)issued + 1u);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (of a pair: the even CTA's) ----------------
@@ -359,6 +365,7 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
             else
               umma_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
           }
+          ++issued;
           if (PAIR)
             umma2_commit(bar_empty(at.s), both);
           else
@@ -530,10 +537,40 @@ i8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant
   // ---- teardown ----
   tc_fence_before();
   __syncwarp();
-  if (PAIR)
-    cluster_barrier();  // neither CTA leaves while the pair's MMAs, copies or arrivals may touch it
-  else
+  __syncthreads();
+  // Where a wait has expired, this CTA's copies and MMAs may be under way still (on the normal
+  // path the MMAs have waited for the copies, and the epilogue for the MMAs, of both CTAs of a
+  // pair): they end before anything is freed. The even CTA sees to the pair's.
+  if (*abort_flag && r == 0) {
+    if (warp == 0 && lane == 0) {
+      const int drop = g_test_drop_stage;
+      auto drain = [&](int from, int to, bool odd_only) {
+        for (int i = max(from, 0); i < to; ++i) {
+          if (i == drop) continue;
+          if (odd_only) mbar_arrive_expect_tx(bar_full(i % p.stages), stage_bytes);
+          mbar_wait_drain(bar_full(i % p.stages), (uint32_t)(i / p.stages) & 1u);
+        }
+      };
+      drain(issued - p.stages, issued, false);
+      if (PAIR) {  // stages of which the odd CTA alone has issued its half
+        const uint64_t t0 = global_timer_ns();
+        uint32_t odd;
+        // (it gives up a limit later than this one at most; waits look at the time every millisecond)
+        while ((odd = ld_acquire_cluster_u32(odd_issued)) == 0u && global_timer_ns() - t0 < limit + 5000000u) {}
+        drain(issued, (int)odd - 1, true);
+      }
+    }
+    if (warp == 1 && lane == 0 && issued) {
+      if (PAIR)
+        umma2_commit(bar_done, (uint16_t)(1u << leader));
+      else
+        umma_commit(bar_done);
+      mbar_wait_drain(bar_done, 0);
+    }
+    __syncwarp();
     __syncthreads();
+  }
+  if (PAIR) cluster_barrier();  // neither CTA leaves while the pair's MMAs, copies or arrivals may touch it
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();

@@ -307,7 +307,7 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   constexpr int C = kMi8Cluster[DOWN];
   extern __shared__ uint8_t smem_raw[];
   __shared__ Mi8Route<PL> r;
-  __shared__ __align__(8) uint64_t bar_mem[3 * kMi8MaxStages + 4];
+  __shared__ __align__(8) uint64_t bar_mem[3 * kMi8MaxStages + 5];
   // scale and its inverse: kernel 1 of each token, kernel 2 of each row of h
   __shared__ float2 s_scale[DOWN ? kMi8MaxRows : kMi8MaxM];
   __shared__ uint32_t tmem_slot_mem;
@@ -323,6 +323,7 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   auto bar_empty = [&](int s) { return bars + 8u * (2 * kMi8MaxStages + s); };
   auto bar_tfull = [&](int a) { return bars + 8u * (3 * kMi8MaxStages + a); };
   auto bar_tempty = [&](int a) { return bars + 8u * (3 * kMi8MaxStages + 2 + a); };
+  const uint32_t bar_done = bars + 8u * (3 * kMi8MaxStages + 4);  // issued MMAs have ended (on expiry)
   volatile int* abort_flag = &abort_mem;
 
   if (threadIdx.x == 0) {
@@ -335,6 +336,7 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
       mbar_init(bar_tfull(a), 1);
       mbar_init(bar_tempty(a), 4);
     }
+    mbar_init(bar_done, 1);
     abort_mem = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -384,20 +386,20 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   auto columns = [&](int u) { return (4 * (r.group_row[group_of(u)] >> 16) + 15) / 16 * 16; };
 
   const uint64_t limit = *const_cast<volatile unsigned long long*>(&g_wait_limit_ns);
+  int issued = 0;  // by a role's one thread: stages copied (warp 0), consumed (warp 1)
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (lane == 0) {
       const int drop = g_test_drop_stage;  // test hook; -1 in normal use
-      int it = 0;
       I8Ring at;
       bool ok = true;
       for (int u = first; u < units && ok; u += step) {
         const int e = r.group_expert[group_of(u)];
-        for (int k = 0; k < nk; ++k, ++it, at.next(p.stages)) {
+        for (int k = 0; k < nk; ++k, ++issued, at.next(p.stages)) {
           const int s = at.s;
           // (a barrier's phase before its first counts as complete)
           if (!(ok = mbar_wait_l(bar_empty(s), at.parity ^ 1, abort_flag, limit))) break;
-          if (it == drop) continue;  // test hook: this stage never arrives
+          if (issued == drop) continue;  // test hook: this stage never arrives
           mbar_arrive_expect_tx(bar_a(s), kI8ATile);
           const uint32_t a_dst = sbase + s * stage_bytes;
           if (DOWN) {
@@ -407,9 +409,6 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
           }
         }
       }
-      if (*abort_flag)  // every issued copy lands before this CTA may exit
-        for (int i = max(0, it - p.stages); i < it; ++i)
-          if (i != drop) mbar_wait_drain(bar_a(i % p.stages), (i / p.stages) & 1);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
@@ -433,6 +432,7 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
 #pragma unroll
           for (int kk = 0; kk < kI8KB / 32; ++kk)  // 32 bytes of K on: 2 in the descriptors' units
             umma_i8(d, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) != 0);
+          ++issued;
           umma_commit(bar_empty(at.s));
         }
         if (ok) umma_commit(bar_tfull(a));
@@ -572,6 +572,21 @@ mi8_kernel(const __grid_constant__ CUtensorMap tmap_w, Mi8Params p) {
   // ---- teardown; kernel 2 first sums over the cluster ----
   tc_fence_before();
   __syncthreads();
+  // Where a wait has expired, copies and MMAs may be under way still (on the normal path the MMAs
+  // have waited for the copies, and the epilogue for the MMAs): they end before anything is freed.
+  if (*abort_flag) {
+    if (warp == 0 && lane == 0) {
+      const int drop = g_test_drop_stage;
+      for (int i = max(0, issued - p.stages); i < issued; ++i)
+        if (i != drop) mbar_wait_drain(bar_a(i % p.stages), (uint32_t)(i / p.stages) & 1u);
+    }
+    if (warp == 1 && lane == 0 && issued) {
+      umma_commit(bar_done);
+      mbar_wait_drain(bar_done, 0);
+    }
+    __syncwarp();
+    __syncthreads();
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();

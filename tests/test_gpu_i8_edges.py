@@ -159,3 +159,22 @@ def test_gemm_most_tokens():
         assert torch.equal(Y[rows].view(-1, 1024), acc * sx[rows].view(-1, 1024) * sw)
     del X, sx, Y
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------ waits that run out
+
+@pytest.mark.parametrize("drop", [1, 3, 5, 9])
+def test_moe_waits_run_out_part_of_the_way(drop):
+    """A later stage never arrives in either kernel, with copies ahead of it and products behind."""
+    L, Wg, sg, Wd, sd, X = moe_inputs(66, 12, 24, 1040, 784)
+    case = (L, 4, Wg, sg, Wd, sd, X)
+    good = q.moe_i8_layer(*case)
+    assert q.q4k_last_device_status() == 0
+    try:
+        q.q4k_test_wait_fault(drop, 200_000)
+        q.moe_i8_layer(*case)
+        assert q.q4k_last_device_status() == 7  # Q4K_ERR_DEVICE_TIMEOUT
+    finally:
+        q.q4k_test_wait_fault(-1, 0)
+    assert torch.equal(q.moe_i8_layer(*case), good)
+    assert q.q4k_last_device_status() == 0

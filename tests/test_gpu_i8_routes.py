@@ -147,3 +147,23 @@ def test_waits_of_pairs_run_out_and_recover(M, N, K, act):
         q.q4k_test_wait_fault(-1, 0)
     assert torch.equal(q.i8_gemm(*args, act=act), good)
     assert q.q4k_last_device_status() == 0
+
+
+@pytest.mark.parametrize("drop", [1, 5, 9])
+@pytest.mark.parametrize("M,N,K,act", [(605, 20980, 304, 0), (457, 25752, 320, 1), (2048, 17408, 5120, 0), (271, 3486, 4240, 0),
+                                       (35, 32250, 112, 0), (5, 300, 2064, 0)])
+def test_waits_run_out_part_of_the_way(M, N, K, act, drop):
+    """A later stage never arrives, with tiles behind and copies ahead of it."""
+    g = _gen(6)
+    args = (codes(g, N, K), scales(g, N) / 100, codes(g, M, K), scales(g, M))
+    good = q.i8_gemm(*args, act=act)
+    assert q.q4k_last_device_status() == 0
+    try:
+        q.q4k_test_wait_fault(drop, 200_000)
+        q.i8_gemm(*args, act=act)
+        late = q.q4k_last_device_status()
+    finally:
+        q.q4k_test_wait_fault(-1, 0)
+    assert late in (0, 7)  # (0: no CTA has that many stages)
+    assert torch.equal(q.i8_gemm(*args, act=act), good)
+    assert q.q4k_last_device_status() == 0
