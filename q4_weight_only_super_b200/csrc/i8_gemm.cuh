@@ -31,7 +31,7 @@
 // tokens 68 us (2.7 POPS), at one token 29.5 us (6.0 TB/s, 92% of the measured copy rate); 5120 x
 // 17408 at eight tokens 18.1 us (split over six CTAs; unsplit 40), at 300 tokens 29.7 us. Called one
 // after the other for longer, the power cap lowers the clock of the products that keep the
-// tensor pipe busy: 285, 80 and 34 us at 4096, 512 and 300 tokens.
+// tensor pipe busy: 286, 82 and 35 us at 4096, 512 and 300 tokens.
 // SwiGLU tiles hold 64 gate and the matching 64 up rows, 16 of each per warp's 32 lanes, so
 // that one shuffle brings a gate and its up value together.
 // Every wait is bounded; on expiry the kernel latches Q4K_ERR_DEVICE_TIMEOUT, stops all
